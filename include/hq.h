@@ -51,7 +51,8 @@
  * decoded tile is not a canonical tile: its output is zero), HQ_ST_TIMEOUT
  * (a bounded wait between thread blocks gave up: the call's output is
  * invalid), HQ_ST_RANGE (the integer product saturated a doubled lattice
- * coordinate to +-127).
+ * coordinate to +-127), HQ_ST_INDEX (a slot, page or sequence description
+ * points outside its array: what it names is skipped).
  *
  * The same seed must be given to encode and decode: signs and dither are
  * regenerated from it, not stored.
@@ -83,7 +84,8 @@ enum {
 };
 
 /* device status bits OR-ed into *d_status */
-enum { HQ_ST_NONFINITE = 1, HQ_ST_CAPACITY = 2, HQ_ST_CORRUPT = 4, HQ_ST_TIMEOUT = 8, HQ_ST_RANGE = 16 };
+enum { HQ_ST_NONFINITE = 1, HQ_ST_CAPACITY = 2, HQ_ST_CORRUPT = 4, HQ_ST_TIMEOUT = 8, HQ_ST_RANGE = 16,
+       HQ_ST_INDEX = 32 };
 
 /* A compressed matrix.  Host struct; all pointers are device memory owned by
  * the caller.
@@ -366,6 +368,174 @@ int hq_kv_attention(const hq_stream *k, const hq_stream *v, int64_t heads, int64
                     int head_dim, int group, int lattice, float bps_k, float bps_v, uint64_t seed_k,
                     uint64_t seed_v, const void *q, float scale, float *out, void *workspace,
                     uint64_t workspace_bytes, void *stream, int32_t *d_status);
+
+/* hq_kv_attention that also writes lse (device fp32 [heads * group], may be
+ * NULL): log sum_t exp(scale <q, k_hat_t>) of each query head, minus infinity
+ * for tokens == 0.  With it hq_attention_merge joins the result over a
+ * compressed history with the result over recent pages. */
+int hq_kv_attention_lse(const hq_stream *k, const hq_stream *v, int64_t heads, int64_t tokens,
+                        int head_dim, int group, int lattice, float bps_k, float bps_v, uint64_t seed_k,
+                        uint64_t seed_v, const void *q, float scale, float *out, float *lse,
+                        void *workspace, uint64_t workspace_bytes, void *stream, int32_t *d_status);
+
+/* ------------------------------------------------------------------
+ * Serving beside the codec: rotary positions, a paged cache of recent keys
+ * and values, attention over it, and the join with the compressed history.
+ * A page laid out as one slab of page_size vectors per KV head (the default
+ * strides) is what hq_kv_encode takes, so a full page is compressed where it
+ * lies.  The pages read for the codec name no serving path: these operators
+ * follow their formulas, given at each.
+ *
+ * hq_rows is a [tokens][heads][head_dim] array: element (t, h, i) at
+ * p[t token_stride + h head_stride + i].  p is 16-byte aligned device memory,
+ * strides are >= 0 and multiples of 16 bytes; a stride along an extent of one
+ * is not used.  Rows of an output must not overlap (HQ_ERR_ARG). */
+typedef struct hq_rows {
+    void *p;
+    int32_t dtype;                      /* HQ_BF16 or HQ_F32 */
+    int64_t token_stride, head_stride;  /* elements */
+} hq_rows;
+
+/* A pool of bf16 pages: vector (page, head h, slot i) of K at
+ * k[page page_stride + h head_stride + i slot_stride], head_dim contiguous
+ * elements; V the same from v.  16-byte aligned, strides positive multiples of
+ * 8 elements, vectors not overlapping.  page_size a power of two from 16 to
+ * 1024; head_dim 64, 128 or 256; heads <= 65535; pages < 2^31 / page_size. */
+typedef struct hq_pages {
+    void *k, *v;
+    int64_t pages;
+    int32_t page_size, heads, head_dim;
+    int64_t page_stride, head_stride, slot_stride;  /* elements */
+} hq_pages;
+
+/* How a rotation made for `original` positions is stretched to longer
+ * contexts.  theta_i = base^(-2 i / rotary_dim) is the angle per position of
+ * pair i, i < rotary_dim / 2:
+ *   HQ_ROPE_PLAIN   theta_i
+ *   HQ_ROPE_LINEAR  theta_i / factor (positions interpolated)
+ *   HQ_ROPE_NTK     base replaced by base factor^(rotary_dim / (rotary_dim - 2))
+ *   HQ_ROPE_BANDS   by the turns n_i = original theta_i / 2 pi a pair makes in
+ *                   the original context: theta_i / factor below `low` turns,
+ *                   theta_i above `high`, linear in n_i between
+ *   HQ_ROPE_YARN    "YaRN" (Peng, Quesnelle, Fan, Shippole 2023): theta_i /
+ *                   factor below `low` turns, theta_i above `high`, linear in
+ *                   the pair's number between (the border pairs rounded
+ *                   outwards), amplitude 0.1 ln(factor) + 1 */
+enum { HQ_ROPE_PLAIN = 0, HQ_ROPE_LINEAR = 1, HQ_ROPE_NTK = 2, HQ_ROPE_BANDS = 3, HQ_ROPE_YARN = 4 };
+typedef struct hq_rope_scaling {
+    int32_t kind;
+    double factor;     /* > 0 (HQ_ROPE_YARN: >= 1) */
+    double low, high;  /* turns, 0 < low < high (BANDS, YARN) */
+    double original;   /* positions of the original context, > 0 (BANDS, YARN) */
+} hq_rope_scaling;
+
+/* Pairs: (i, i + rotary_dim / 2), or (2 i, 2 i + 1) */
+enum { HQ_ROPE_HALF = 0, HQ_ROPE_INTERLEAVED = 1 };
+
+/* theta_i of rotary_dim / 2 pairs in binary64 (theta, host) and the amplitude
+ * of the rotation.  rotary_dim a multiple of 16 from 16 to 256, base > 1;
+ * scaling NULL is HQ_ROPE_PLAIN.  Host only. */
+int hq_rope_frequencies(int rotary_dim, double base, const hq_rope_scaling *scaling, double *theta,
+                        float *amplitude);
+
+/* turns[i] = theta_i / 2 pi modulo one turn, in units of 2^-64 turns: the form
+ * the kernels take, with which p turns[i] modulo 2^64 is the angle of
+ * position p without rounding.  HQ_ERR_ARG for a theta that is not finite.
+ * Host only: the caller copies the table to the device. */
+int hq_rope_table(const double *theta, int pairs, uint64_t *turns);
+
+/* Rotary positions: for every token t and head, with a = positions[t] theta_i
+ * (inverse: -a), pair (x1, x2) of the first rotary_dim elements becomes
+ *   amplitude (x1 cos a - x2 sin a, x2 cos a + x1 sin a)
+ * and the other elements are copied.  Arithmetic in binary32, rounded once to
+ * y's type.  The inverse is the transpose: it undoes a rotation of amplitude 1
+ * and is the gradient of the forward call.
+ *   x, y       [tokens][heads][head_dim], each HQ_BF16 or HQ_F32; y may be x
+ *              itself (same strides and type), any other overlap is undefined
+ *   head_dim   a multiple of 16 from 16 to 256; heads <= 65535, tokens < 2^31
+ *   positions  device int64 [tokens], any sign
+ *   turns      device, rotary_dim / 2 entries; rotary_dim a multiple of 16 up
+ *              to head_dim */
+int hq_rope(const hq_rows *x, const hq_rows *y, int64_t tokens, int heads, int head_dim,
+            const int64_t *positions, const uint64_t *turns, int rotary_dim, int layout,
+            float amplitude, int inverse, void *stream);
+
+/* Append new tokens to the paged cache: k (rotated as by hq_rope) and v go to
+ * slot slots[t] = page * page_size + offset of every KV head, rounded once to
+ * bf16; q, if given, is rotated into q_out in the same launch.
+ *   q, q_out   [tokens][q_heads][head_dim]; both NULL with q_heads = 0
+ *   k, v       [tokens][pages->heads][pages->head_dim]
+ *   turns      NULL with rotary_dim = 0: nothing is rotated (positions unused)
+ *   slots      device int64 [tokens].  A negative slot skips the token (its
+ *              q_out row is left as it was); one past the pool skips it and
+ *              raises HQ_ST_INDEX.  The slots of one call must be distinct:
+ *              a slot named twice holds elements of either token. */
+int hq_kv_append(const hq_rows *q, const hq_rows *q_out, int q_heads, const hq_rows *k, const hq_rows *v,
+                 int64_t tokens, const int64_t *positions, const uint64_t *turns, int rotary_dim,
+                 int layout, float amplitude, const int64_t *slots, const hq_pages *pages, void *stream,
+                 int32_t *d_status);
+
+/* Bytes of device workspace hq_paged_attention needs for these bounds (tile
+ * counts, block shares, counters and partial results).  Depends on the SM
+ * count of the current device.  Host only. */
+int hq_paged_attention_workspace_bytes(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_kv,
+                                       int heads, int head_dim, int group, uint64_t *out);
+
+/* Attention of new tokens over the paged cache, a batch of sequences at once:
+ * sequence b has q_len = q_start[b + 1] - q_start[b] new tokens (one when
+ * decoding, a chunk of a prompt otherwise), rows q_start[b] .. of q, and
+ * kv_len[b] cached tokens, these new ones included; token j of it stands at
+ * position p = kv_len[b] - q_len + j.  For query head qh = h * group + g:
+ *   out[j][qh] = sum_t w_t v_t / sum_t w_t,  w_t = exp(scale <q, k_t>),
+ *   lse[j][qh] = log sum_t w_t
+ * over the cached tokens t with t <= p (causal) and t > p - window (window >
+ * 0).  A row that sees no token is zero with lse minus infinity.  Products run
+ * on the tensor cores with bf16 operands and binary32 sums; the weights are
+ * rounded to bf16 for the product with v, their sum is not.
+ *   q            bf16 [tokens][heads * group][head_dim]
+ *   q_start      device int32 [batch + 1], non-decreasing, within 0 .. tokens;
+ *                rows of out outside every sequence are left as they were
+ *   kv_len       device int32 [batch], >= 0; may be below q_len (the first
+ *                rows then see nothing)
+ *   max_q, max_kv  bounds of q_len and kv_len
+ *   pages, table   token t of sequence b is slot t % page_size of page
+ *                table[b table_stride + t / page_size] (device int32, entries
+ *                past the last token are not read).  A page may serve several
+ *                sequences.  A page outside the pool counts as zero vectors
+ *                and raises HQ_ST_INDEX.  Slots past kv_len are never used,
+ *                whatever they hold; vectors within it should be finite (a
+ *                NaN or infinity may reach every row of the same sequence and
+ *                KV head, masked or not).
+ *   scale        finite, any sign
+ *   causal       0: every new token sees all kv_len tokens (window still
+ *                counts from its position)
+ *   out          [tokens][heads * group][head_dim], HQ_BF16 or HQ_F32
+ *   lse          fp32 [tokens][heads * group] or NULL
+ *   workspace    device, >= hq_paged_attention_workspace_bytes, 16-byte
+ *                aligned; overwritten, so calls sharing one must be ordered
+ * A sequence that is inconsistent (q_start out of order or outside the rows,
+ * q_len > max_q, kv_len > max_kv or past its row of the table) is skipped and
+ * raises HQ_ST_INDEX.  batch < 2^24, heads * group <= 65535, max_q * group <
+ * 2^30, max_kv <= 2^30, tokens < 2^31.  The result does not depend on timing. */
+int hq_paged_attention(const hq_rows *q, const int32_t *q_start, const int32_t *kv_len, int64_t batch,
+                       int64_t tokens, int64_t max_q, int64_t max_kv, int group, const hq_pages *pages,
+                       const int32_t *table, int64_t table_width, int64_t table_stride, float scale,
+                       int causal, int64_t window, const hq_rows *out, float *lse, void *workspace,
+                       uint64_t workspace_bytes, void *stream, int32_t *d_status);
+
+/* Join two partial attention results over disjoint sets of cached tokens:
+ *   out = (w_a a + w_b b) / (w_a + w_b),  w = exp(lse - max(lse_a, lse_b)),
+ *   lse = log(exp(lse_a) + exp(lse_b))
+ * a, b, out  [tokens][heads][head_dim], each HQ_BF16 or HQ_F32, head_dim a
+ *            multiple of 8 up to 1024; lse_a, lse_b, lse fp32 [tokens][heads]
+ *            (lse may be NULL).  A part whose lse is minus infinity is not
+ *            read; if both are, the row is zero.  out may be a or b themselves
+ *            (same strides and type); lse must be neither lse_a nor lse_b
+ *            (HQ_ERR_ARG: other threads still read them).
+ * tokens * heads < 2^32. */
+int hq_attention_merge(const hq_rows *a, const float *lse_a, const hq_rows *b, const float *lse_b,
+                       int64_t tokens, int heads, int head_dim, const hq_rows *out, float *lse,
+                       void *stream);
 
 /* Testing hook for failure detection (no counterpart on the pages): hq_encode
  * in which the chunk of tiles numbered `stalled_chunk` (in encode-chunk order)

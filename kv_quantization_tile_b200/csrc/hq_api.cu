@@ -571,6 +571,15 @@ int hq_kv_attention(const hq_stream *k, const hq_stream *v, int64_t heads, int64
                     const void *q, float scale, float *out, void *workspace, uint64_t workspace_bytes,
                     void *stream, int32_t *d_status)
 {
+    return hq_kv_attention_lse(k, v, heads, tokens, head_dim, group, lattice, bps_k, bps_v, seed_k, seed_v, q, scale,
+                               out, nullptr, workspace, workspace_bytes, stream, d_status);
+}
+
+int hq_kv_attention_lse(const hq_stream *k, const hq_stream *v, int64_t heads, int64_t tokens, int head_dim,
+                        int group, int lattice, float bps_k, float bps_v, uint64_t seed_k, uint64_t seed_v,
+                        const void *q, float scale, float *out, float *lse, void *workspace,
+                        uint64_t workspace_bytes, void *stream, int32_t *d_status)
+{
     if (heads < 0 || tokens < 0 || !valid_head_dim(head_dim) || group < 1 || !std::isfinite(scale))
         return HQ_ERR_ARG;
     if (heads > 65535 || tokens >= (int64_t)1 << 32 || group > 65535 * 8) return HQ_ERR_UNSUPPORTED;
@@ -583,10 +592,12 @@ int hq_kv_attention(const hq_stream *k, const hq_stream *v, int64_t heads, int64
     if ((a.k.slot != 0) != (a.v.slot != 0)) return HQ_ERR_UNSUPPORTED;  // K and V of one kind
     if (heads == 0) return HQ_OK;
     cudaStream_t s = (cudaStream_t)stream;
-    if (!out || !aligned(out, 16)) return HQ_ERR_ARG;
-    if (tokens == 0)
-        return cudaMemsetAsync(out, 0, sizeof(float) * (size_t)(heads * group * head_dim), s) == cudaSuccess
-                   ? HQ_OK : HQ_ERR_CUDA;
+    if (!out || !aligned(out, 16) || !aligned(lse, 4)) return HQ_ERR_ARG;
+    if (tokens == 0) {
+        if (cudaMemsetAsync(out, 0, sizeof(float) * (size_t)(heads * group * head_dim), s) != cudaSuccess)
+            return HQ_ERR_CUDA;
+        return !lse || launch_fill(lse, heads * group, -INFINITY, s) == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
+    }
     if (!q || !aligned(q, 16)) return HQ_ERR_ARG;
     const AttnWorkspace w = attention_workspace(heads, tokens, head_dim, group);
     if (!workspace || !aligned(workspace, 16) || workspace_bytes < w.total_bytes) return HQ_ERR_WORKSPACE;
@@ -599,6 +610,7 @@ int hq_kv_attention(const hq_stream *k, const hq_stream *v, int64_t heads, int64
     a.tokens = tokens;
     a.group = group;
     a.scale = scale;
+    a.lse = lse;
     a.status = d_status;
     return launch_attention(head_dim, lattice, a, s) == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
 }

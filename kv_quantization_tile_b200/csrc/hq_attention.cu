@@ -298,6 +298,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_min_blocks(N, GB)) kv_atten
         if (lane == 0) {
             sM[warp] = M;
             sL[warp] = L;
+            if (a.lse) a.lse[qh0 + warp] = M + logf(L);
         }
     }
     __syncthreads();
@@ -357,7 +358,19 @@ __global__ void __launch_bounds__(kAttnThreads, attn_min_blocks(N, GB)) kv_atten
     }
 }
 
+__global__ void fill_kernel(float *p, int64_t n, float v)
+{
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) p[i] = v;
+}
+
 // ------------------------------------------------------------------ launch
+cudaError_t launch_fill(float *p, int64_t n, float v, cudaStream_t s)
+{
+    const int64_t blocks = (n + 255) / 256;
+    fill_kernel<<<(unsigned)(blocks < 1024 ? blocks : 1024), 256, 0, s>>>(p, n, v);
+    return cudaGetLastError();
+}
+
 namespace {
 
 // Coordinates per lane of a parsed tile.

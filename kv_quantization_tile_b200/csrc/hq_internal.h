@@ -87,6 +87,7 @@ struct AttnArgs {
     int group;              // query heads per KV head
     int splits, tokens_per_split;
     float scale;
+    float *lse;             // fp32 [heads * group] or null
     int32_t *status;
 };
 
@@ -135,6 +136,7 @@ cudaError_t launch_stats(int tile, int lattice, const DecodeArgs &a, uint64_t *c
                          cudaStream_t s);
 // Fills a.splits / a.tokens_per_split from the kernel's occupancy, then launches.
 cudaError_t launch_attention(int head_dim, int lattice, AttnArgs a, cudaStream_t s);
+cudaError_t launch_fill(float *p, int64_t n, float v, cudaStream_t s);
 
 // Query heads one attention block serves (1, 2, 4 or 8), and the token
 // splits for `blocks_per_sm` resident blocks (every split non-empty; never

@@ -1,0 +1,296 @@
+// hq_paged.h -- argument blocks, launchers and shared device code of the
+// serving operators: rotary positions, the append to a paged KV cache,
+// attention over it and the join of two partial attention results (not part
+// of the public ABI).
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "hq_internal.h"
+
+namespace hq {
+
+constexpr int kStatusIndex = 32;
+
+// A [tokens][heads][head_dim] array; strides in elements.
+struct Rows {
+    void *p;
+    int64_t ts, hs;
+    int f32;  // binary32 elements (else bf16)
+};
+
+// ------------------------------------------------------------ positions
+// Rotation and append: `heads` rows of `x` (queries) go to `y`; if kvh > 0,
+// kvh rows of k (rotated) and v (copied) go to the page pool.
+struct PosArgs {
+    Rows x, y, k, v;
+    int64_t tokens;
+    int heads, kvh, head_dim, rotary;  // rotary: rotated elements per head (0: none)
+    int interleaved, inverse;
+    float amplitude;
+    const int64_t *positions;
+    const uint64_t *turns;             // theta / 2 pi in 2^-64 turns, rotary / 2 entries
+    const int64_t *slots;              // null: no append
+    uint16_t *pk, *pv;
+    int64_t page_stride, head_stride, slot_stride, nslots;
+    int page_shift;
+    int tokens_per_block;
+    FastDiv items_div, unit_div;       // by items per token, by items per head
+    int32_t *status;
+};
+
+cudaError_t launch_positions(const PosArgs &a, cudaStream_t s);
+
+// ------------------------------------------------------------ join
+struct MergeArgs {
+    Rows a, b, out;
+    const float *lse_a, *lse_b;  // [tokens][heads]
+    float *lse;                  // may be null
+    int64_t tokens;
+    int heads, head_dim;
+    FastDiv heads_div;
+};
+
+cudaError_t launch_merge(const MergeArgs &a, cudaStream_t s);
+
+// ------------------------------------------------------------ attention
+// Where a block's share of the tiles begins (written by the plan kernel).
+struct PagedStart {
+    int32_t b, h, rt, tile;  // sequence, KV head, row tile, tile within the job
+};
+
+struct PagedArgs {
+    Rows q, out;
+    float *lse;              // [tokens][heads * group]; may be null
+    const int32_t *q_start, *kv_len, *table;
+    int64_t table_stride;
+    int64_t tokens;
+    int batch, max_q, max_tokens;  // max_tokens: tokens a row of the table can hold
+    int heads, group;
+    FastDiv group_div;
+    const uint16_t *k, *v;
+    int64_t page_stride, head_stride, slot_stride;
+    uint32_t pages;
+    int page_shift;
+    float scale_log2;        // |scale| log2 e
+    int q_mode;              // 0: q, 1: -q (negative scale), 2: zeros (scale 0)
+    int causal;
+    int window;              // positions a query sees, itself included (0: all)
+    int row_lo, row_hi;      // sequences with row_lo < q_len * group <= row_hi
+    // plan (workspace)
+    int64_t *prefix;         // [batch + 1] tiles before each sequence
+    PagedStart *start;       // [grid]
+    uint32_t *counter;       // [grid] finished parts of the job whose first tile block c holds
+    float *part;             // [2 grid] partial results
+    int grid, min_tiles;     // blocks; least tiles a block takes
+    int32_t *status;
+};
+
+// Sizes a launch needs.
+struct PagedPlan {
+    int grid_few, rows_few;     // mma.sync kernel: blocks, rows per row tile
+    int grid_many, rows_many;   // tcgen05 kernel: blocks (0: not launched), rows per row tile
+    uint64_t prefix_bytes, start_bytes, counter_bytes, part_bytes, total;
+};
+
+PagedPlan paged_plan(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_kv, int heads, int group, int head_dim);
+cudaError_t launch_paged(const PagedArgs &a, const PagedPlan &p, int head_dim, void *workspace, cudaStream_t s);
+
+#ifdef __CUDACC__
+// ------------------------------------------------------------ device side
+// One sequence as a kernel sees it.
+struct Seq {
+    int q0, nq, kv, rows;
+};
+
+// Sequence b; rows = 0 if it is not this kernel's, empty, or inconsistent
+// (offsets out of order or past the rows, more new tokens than max_q, more
+// cached tokens than its row of the table holds: `bad`).
+__device__ __forceinline__ Seq load_seq(const PagedArgs &a, int b, bool &bad)
+{
+    Seq s;
+    s.q0 = a.q_start[b];
+    const int q1 = a.q_start[b + 1];
+    s.kv = a.kv_len[b];
+    bad = s.q0 < 0 || q1 < s.q0 || q1 > a.tokens || q1 - s.q0 > a.max_q || s.kv < 0 || s.kv > a.max_tokens;
+    s.nq = bad ? 0 : q1 - s.q0;
+    s.rows = s.nq * a.group;
+    if (s.rows <= a.row_lo || s.rows > a.row_hi) s.rows = 0;
+    return s;
+}
+
+// First and last + 1 cached token that any of the new tokens j0 .. j1 of a
+// sequence sees.
+__device__ __forceinline__ void seen_range(const PagedArgs &a, const Seq &s, int j0, int j1, int &lo, int &hi)
+{
+    const int64_t first = (int64_t)s.kv - s.nq;
+    int64_t l = a.window ? first + j0 + 1 - a.window : 0, h = a.causal ? first + j1 + 1 : s.kv;
+    if (l < 0) l = 0;
+    if (h > s.kv) h = s.kv;
+    if (h < 0) h = 0;
+    if (l > h) l = h;
+    lo = (int)l;
+    hi = (int)h;
+}
+
+// Tiles [t0, t0 + n) of T tokens that row tile rt (RT packed rows) reads; a
+// job always has one tile at least (it writes its rows even if they see nothing).
+template <int T, int RT>
+__device__ __forceinline__ void job_tiles(const PagedArgs &a, const Seq &s, int rt, int &t0, int &n, int &lo, int &hi)
+{
+    const int r0 = rt * RT, r1 = min(r0 + RT, s.rows) - 1;
+    seen_range(a, s, (int)fast_div((uint32_t)r0, a.group_div), (int)fast_div((uint32_t)r1, a.group_div), lo, hi);
+    t0 = lo / T;
+    n = (hi + T - 1) / T - t0;
+    if (n < 1) n = 1;
+}
+
+// The block's walk over its share of the tiles: segments of jobs (sequence,
+// KV head, row tile), in the order sequence, KV head, row tile, tile.
+template <int T, int RT>
+struct SegWalk {
+    Seq s;
+    int b, h, rt, nrt;
+    int t0, n, lo, hi;    // the job's tiles and cached range
+    int first, count;     // the segment: tiles t0 + first .. + count
+    int64_t at, end, total;
+    int grid;
+
+    __device__ __forceinline__ bool begin(const PagedArgs &a)
+    {
+        total = a.prefix[a.batch];
+        const int64_t most = (total + a.min_tiles - 1) / a.min_tiles;
+        grid = (int)min((int64_t)a.grid, most);
+        const int c = blockIdx.x;
+        if (c >= grid) return false;
+        at = total * c / grid;
+        end = total * (c + 1) / grid;
+        const PagedStart st = a.start[c];
+        b = st.b;
+        h = st.h;
+        rt = st.rt;
+        first = st.tile;
+        bool bad;
+        s = load_seq(a, b, bad);
+        nrt = (s.rows + RT - 1) / RT;
+        job_tiles<T, RT>(a, s, rt, t0, n, lo, hi);
+        count = (int)min((int64_t)(n - first), end - at);
+        return true;
+    }
+
+    __device__ __forceinline__ bool next(const PagedArgs &a)
+    {
+        at += count;
+        if (at >= end) return false;
+        first = 0;
+        if (++rt == nrt) {
+            rt = 0;
+            if (++h == a.heads) {
+                h = 0;
+                bool bad;
+                do {
+                    if (++b >= a.batch) return false;
+                    s = load_seq(a, b, bad);
+                } while (s.rows == 0);
+                nrt = (s.rows + RT - 1) / RT;
+            }
+        }
+        job_tiles<T, RT>(a, s, rt, t0, n, lo, hi);
+        count = (int)min((int64_t)n, end - at);
+        return true;
+    }
+
+    __device__ __forceinline__ bool whole() const { return count == n; }
+    __device__ __forceinline__ int block_of(int64_t g) const { return (int)(((g + 1) * grid - 1) / total); }
+    // blocks that hold a part of this job
+    __device__ __forceinline__ int owner() const { return block_of(at - first); }
+    __device__ __forceinline__ int last() const { return block_of(at - first + n - 1); }
+    // a block's parts: one that begins inside a job, one that begins with it
+    __device__ __forceinline__ int slot() const { return 2 * (int)blockIdx.x + (first == 0 ? 1 : 0); }
+};
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// ------------------------------------------------------------ results
+// Elements 4 c .. 4 c + 3 of packed row r of a job, from its unnormalised sum,
+// maximum (powers of two) and weight sum; a row that saw nothing is zero.
+__device__ __forceinline__ void finish_row(const PagedArgs &a, int q0, int h, int r, int c, float4 v, float m, float l)
+{
+    const int j = (int)fast_div((uint32_t)r, a.group_div), head = h * a.group + r - j * a.group;
+    const int64_t tok = q0 + j, off = tok * a.out.ts + head * a.out.hs + 4 * c;
+    const float f = l == 0.0f ? 0.0f : 1.0f / l;
+    if (l == 0.0f) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (a.out.f32) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.out.p) + off) =
+            make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+    } else {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * f, v.y * f), hi = __floats2bfloat162_rn(v.z * f, v.w * f);
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out.p) + off) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+    }
+    if (c == 0 && a.lse)
+        a.lse[tok * (a.heads * a.group) + head] = l == 0.0f ? -INFINITY : fmaf(m, 0.693147180559945309f, logf(l));
+}
+
+// A part: m of RT rows, l of RT rows, then RT x D sums.
+template <int RT, int D>
+__device__ __forceinline__ const float *part_of(const PagedArgs &a, int c, int c0)
+{
+    return a.part + (int64_t)(2 * c + (c == c0 ? 1 : 0)) * (RT * (D + 2));
+}
+
+// Join the parts that blocks c0 .. c1 left of row r (packed row pr), columns
+// 4 c .. 4 c + 3, in block order.
+template <int RT, int D>
+__device__ __forceinline__ void join_parts(const PagedArgs &a, int q0, int h, int pr, int r, int c, int c0, int c1)
+{
+    float mt = -INFINITY;
+#pragma unroll 8
+    for (int k = c0; k <= c1; k++) mt = fmaxf(mt, __ldcg(part_of<RT, D>(a, k, c0) + r));
+    const float base = mt == -INFINITY ? 0.0f : mt;
+    float l = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (int k = c0; k <= c1; k++) {
+        const float *p = part_of<RT, D>(a, k, c0);
+        const float f = ex2(__ldcg(p + r) - base);
+        l = fmaf(f, __ldcg(p + RT + r), l);
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p + 2 * RT + r * D + 4 * c));
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
+    }
+    finish_row(a, q0, h, pr, c, acc, mt, l);
+}
+
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Launch a kernel that may become resident before the one in front of it ends
+// (it waits for that one's results with pdl_wait).
+template <typename... P>
+inline cudaError_t launch_dependent(void (*kern)(P...), int grid, int threads, size_t smem, cudaStream_t s, P... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+#endif
+
+}  // namespace hq

@@ -24,7 +24,7 @@ if not os.path.exists(_LIB_PATH):
 HQ_Z, HQ_A2, HQ_D4, HQ_E8 = 1, 2, 4, 8
 HQ_BF16, HQ_F32 = 0, 1
 HQ_OK, HQ_ERR_ARG, HQ_ERR_UNSUPPORTED, HQ_ERR_CAPACITY, HQ_ERR_WORKSPACE, HQ_ERR_CUDA, HQ_ERR_FORMAT = range(7)
-HQ_ST_NONFINITE, HQ_ST_CAPACITY, HQ_ST_CORRUPT, HQ_ST_TIMEOUT, HQ_ST_RANGE = 1, 2, 4, 8, 16
+HQ_ST_NONFINITE, HQ_ST_CAPACITY, HQ_ST_CORRUPT, HQ_ST_TIMEOUT, HQ_ST_RANGE, HQ_ST_INDEX = 1, 2, 4, 8, 16, 32
 LATTICES = {"Z": HQ_Z, "A2": HQ_A2, "D4": HQ_D4, "E8": HQ_E8}
 
 EXPORTS = ["hq_error_string", "hq_version", "hq_rate_constant", "hq_tile_bound_words",
@@ -34,7 +34,13 @@ EXPORTS = ["hq_error_string", "hq_version", "hq_rate_constant", "hq_tile_bound_w
            "hq_decode_gemm", "hq_file_bytes", "hq_file_write", "hq_file_read", "hq_test_gemm_stalled",
            "hq_min_slot_words", "hq_fixed_slot_words", "hq_encode_fixed", "hq_kv_encode_fixed",
            "hq_decode_gemm_int8_workspace_bytes", "hq_decode_gemm_int8", "hq_decode_gemm_fp8",
-           "hq_stream_stats"]
+           "hq_stream_stats", "hq_kv_attention_lse", "hq_rope_frequencies", "hq_rope_table", "hq_rope",
+           "hq_kv_append", "hq_paged_attention_workspace_bytes", "hq_paged_attention", "hq_attention_merge"]
+HQ_ROPE_PLAIN, HQ_ROPE_LINEAR, HQ_ROPE_NTK, HQ_ROPE_BANDS, HQ_ROPE_YARN = range(5)
+HQ_ROPE_HALF, HQ_ROPE_INTERLEAVED = 0, 1
+ROPE_LAYOUTS = {"half": HQ_ROPE_HALF, "interleaved": HQ_ROPE_INTERLEAVED}
+ROPE_SCALINGS = {"plain": HQ_ROPE_PLAIN, "linear": HQ_ROPE_LINEAR, "ntk": HQ_ROPE_NTK, "bands": HQ_ROPE_BANDS,
+                 "yarn": HQ_ROPE_YARN}
 
 
 class hq_file_info(ctypes.Structure):
@@ -48,6 +54,22 @@ class hq_stream(ctypes.Structure):
     _fields_ = [("payload", ctypes.c_void_p), ("payload_capacity_words", ctypes.c_uint64),
                 ("tile_off", ctypes.c_void_p), ("tile_scale", ctypes.c_void_p),
                 ("tile_k", ctypes.c_void_p), ("slot_words", ctypes.c_uint32)]
+
+
+class hq_rows(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class hq_pages(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64)]
+
+
+class hq_rope_scaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("original", ctypes.c_double)]
 
 
 _lib = ctypes.CDLL(_LIB_PATH)
@@ -94,6 +116,21 @@ _SIGS = {
                                   _u64, _vp, _vp]),
     "hq_decode_gemm": (_i32, [ctypes.POINTER(hq_stream), _i64, _i64, _i32, _i32, _f32, _u64, _vp, _i64, _vp, _vp,
                               _u64, _vp, _vp]),
+    "hq_kv_attention_lse": (_i32, [ctypes.POINTER(hq_stream), ctypes.POINTER(hq_stream), _i64, _i64, _i32, _i32,
+                                   _i32, _f32, _f32, _u64, _u64, _vp, _f32, _vp, _vp, _vp, _u64, _vp, _vp]),
+    "hq_rope_frequencies": (_i32, [_i32, ctypes.c_double, ctypes.POINTER(hq_rope_scaling), _vp, ctypes.POINTER(_f32)]),
+    "hq_rope_table": (_i32, [_vp, _i32, _vp]),
+    "hq_rope": (_i32, [ctypes.POINTER(hq_rows), ctypes.POINTER(hq_rows), _i64, _i32, _i32, _vp, _vp, _i32, _i32,
+                       _f32, _i32, _vp]),
+    "hq_kv_append": (_i32, [ctypes.POINTER(hq_rows), ctypes.POINTER(hq_rows), _i32, ctypes.POINTER(hq_rows),
+                            ctypes.POINTER(hq_rows), _i64, _vp, _vp, _i32, _i32, _f32, _vp,
+                            ctypes.POINTER(hq_pages), _vp, _vp]),
+    "hq_paged_attention_workspace_bytes": (_i32, [_i64, _i64, _i64, _i64, _i32, _i32, _i32, ctypes.POINTER(_u64)]),
+    "hq_paged_attention": (_i32, [ctypes.POINTER(hq_rows), _vp, _vp, _i64, _i64, _i64, _i64, _i32,
+                                  ctypes.POINTER(hq_pages), _vp, _i64, _i64, _f32, _i32, _i64,
+                                  ctypes.POINTER(hq_rows), _vp, _vp, _u64, _vp, _vp]),
+    "hq_attention_merge": (_i32, [ctypes.POINTER(hq_rows), _vp, ctypes.POINTER(hq_rows), _vp, _i64, _i32, _i32,
+                                  ctypes.POINTER(hq_rows), _vp, _vp]),
     "hq_kv_attention": (_i32, [ctypes.POINTER(hq_stream), ctypes.POINTER(hq_stream), _i64, _i64, _i32, _i32,
                                _i32, _f32, _f32, _u64, _u64, _vp, _f32, _vp, _vp, _u64, _vp, _vp]),
 }
@@ -445,12 +482,22 @@ def alloc_attention_workspace(heads: int, tokens: int, head_dim: int, group: int
 
 def hq_kv_attention(k: Stream, v: Stream, heads: int, tokens: int, head_dim: int, lattice, bps_k: float,
                     bps_v: float, seed_k: int, seed_v: int, q, scale: float, out, workspace, group: int = 1,
-                    status=None, stream=None):
+                    status=None, stream=None, lse=None):
     """Batch-1 attention of q (bf16 [heads * group, head_dim]) over the KV
-    streams written by hq_kv_encode; out is fp32 [heads * group, head_dim]."""
+    streams written by hq_kv_encode; out is fp32 [heads * group, head_dim].
+    lse (fp32 [heads * group], optional) receives the logarithm of each query
+    head's weight sum, for hq_attention_merge."""
     assert q.dtype == torch.bfloat16 and q.is_contiguous() and q.numel() == heads * group * head_dim
     assert out.dtype == torch.float32 and out.is_contiguous() and out.numel() == heads * group * head_dim
     ks, vs = k.struct(), v.struct()
+    if lse is not None:
+        _need(lse.dtype == torch.float32 and lse.is_contiguous() and lse.numel() == heads * group,
+              "lse: contiguous fp32 [heads * group]")
+        _check(_lib.hq_kv_attention_lse(ctypes.byref(ks), ctypes.byref(vs), heads, tokens, head_dim, group,
+                                        _lat(lattice), bps_k, bps_v, seed_k, seed_v, _ptr(q), scale, _ptr(out),
+                                        _ptr(lse), _ptr(workspace), workspace.numel(), _stream_handle(stream),
+                                        _ptr(status)), "hq_kv_attention_lse")
+        return out
     _check(_lib.hq_kv_attention(ctypes.byref(ks), ctypes.byref(vs), heads, tokens, head_dim, group,
                                 _lat(lattice), bps_k, bps_v, seed_k, seed_v, _ptr(q), scale, _ptr(out),
                                 _ptr(workspace), workspace.numel(), _stream_handle(stream), _ptr(status)),
@@ -468,6 +515,212 @@ def hq_encode_noalloc(x, tile, lattice, bps, seed, out: Stream, status=None, str
     s = out.struct()
     _check(_lib.hq_encode_noalloc(_ptr(x), _dtype_code(x), rows, cols, tile, _lat(lattice), bps, seed,
                                   ctypes.byref(s), _stream_handle(stream), _ptr(status)), "hq_encode_noalloc")
+    return out
+
+
+# ----------------------------------------------------------------- serving
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _on_one_device(*tensors) -> torch.device:
+    """The CUDA device all given tensors (None skipped) lie on."""
+    dev = tensors[0].device
+    _need(dev.type == "cuda", "CUDA tensors only")
+    for t in tensors:
+        _need(t is None or t.device == dev, "tensors on one device only")
+    return dev
+
+
+def _call(fn, dev: torch.device, stream, args, tail=()):
+    """Run fn(*args, stream handle, *tail) with dev current (its context owns the stream)."""
+    with torch.cuda.device(dev):
+        code = fn(*args, _stream_handle(stream), *tail)
+    _check(code, fn.__name__)
+
+
+def _rows(t: torch.Tensor, what: str) -> hq_rows:
+    _need(t.dim() == 3 and (t.stride(2) == 1 or t.numel() == 0), f"{what}: [tokens, heads, head_dim], last stride 1")
+    return hq_rows(t.data_ptr(), _dtype_code(t), t.stride(0), t.stride(1))
+
+
+@dataclass
+class RopeTable:
+    """A rotation of each head's first rotary_dim elements (see rope_table)."""
+    turns: torch.Tensor     # int64 (bit patterns of uint64), rotary_dim / 2: theta / 2 pi in 2^-64 turns
+    rotary_dim: int
+    layout: int             # HQ_ROPE_HALF or HQ_ROPE_INTERLEAVED
+    amplitude: float
+
+
+def hq_rope_frequencies(rotary_dim: int, base: float, scaling: dict | None = None):
+    """(theta float64 array [rotary_dim / 2], amplitude) of a rotation.  scaling:
+    {"kind": "linear" | "ntk" | "bands" | "yarn", "factor": f}, with "original"
+    positions and the turns "low" and "high" for bands, "slow" and "fast" for yarn."""
+    theta = np.zeros(max(rotary_dim // 2, 1), dtype=np.float64)
+    amp = _f32(0)
+    sc = None
+    if scaling is not None:
+        _need(scaling.get("kind") in ROPE_SCALINGS, f"scaling kind: one of {', '.join(ROPE_SCALINGS)}")
+        low, high = ("slow", "fast") if scaling["kind"] == "yarn" else ("low", "high")
+        sc = ctypes.byref(hq_rope_scaling(ROPE_SCALINGS[scaling["kind"]], scaling.get("factor", 1.0),
+                                          scaling.get(low, 0.0), scaling.get(high, 0.0), scaling.get("original", 0.0)))
+    _check(_lib.hq_rope_frequencies(rotary_dim, base, sc, theta.ctypes.data, ctypes.byref(amp)),
+           "hq_rope_frequencies")
+    return theta, amp.value
+
+
+def hq_rope_table(theta) -> np.ndarray:
+    """theta (float64, radians per position) as 2^-64 turns (uint64)."""
+    theta = np.ascontiguousarray(theta, dtype=np.float64)
+    turns = np.zeros(theta.size, dtype=np.uint64)
+    _check(_lib.hq_rope_table(theta.ctypes.data, theta.size, turns.ctypes.data), "hq_rope_table")
+    return turns
+
+
+def rope_table(rotary_dim: int, base: float = 10000.0, scaling: dict | None = None, layout: str = "half",
+               device="cuda") -> RopeTable:
+    """The table hq_rope and hq_kv_append take, made once per model."""
+    _need(layout in ROPE_LAYOUTS, f"layout: one of {', '.join(ROPE_LAYOUTS)}")
+    theta, amplitude = hq_rope_frequencies(rotary_dim, base, scaling)
+    turns = torch.from_numpy(hq_rope_table(theta).view(np.int64)).to(device)
+    return RopeTable(turns, rotary_dim, ROPE_LAYOUTS[layout], amplitude)
+
+
+def _check_rope(positions, rope: RopeTable, tokens: int):
+    _need(positions is not None and positions.dtype == torch.int64 and positions.is_contiguous()
+          and positions.numel() == tokens, "positions: contiguous int64 [tokens]")
+    _need(rope.turns.dtype == torch.int64 and rope.turns.is_contiguous()
+          and rope.turns.numel() == rope.rotary_dim // 2, "rope.turns: contiguous int64 [rotary_dim / 2]")
+
+
+def hq_rope(x, positions, rope: RopeTable, y, inverse: bool = False, stream=None):
+    """Rotate x [tokens, heads, head_dim] (bf16 or fp32, any row strides) at
+    positions (int64 [tokens]) into y (which may be x); inverse turns back."""
+    tokens, heads, d = x.shape
+    _need(y.shape == x.shape, "y: the shape of x")
+    _check_rope(positions, rope, tokens)
+    dev = _on_one_device(x, y, positions, rope.turns)
+    xs, ys = _rows(x, "x"), _rows(y, "y")
+    _call(_lib.hq_rope, dev, stream, (ctypes.byref(xs), ctypes.byref(ys), tokens, heads, d, positions.data_ptr(),
+                                      rope.turns.data_ptr(), rope.rotary_dim, rope.layout, rope.amplitude,
+                                      int(inverse)))
+    return y
+
+
+@dataclass
+class Pages:
+    """A pool of pages: k and v, bf16 [pages, heads, page_size, head_dim] of any
+    strides with contiguous vectors (both the same strides)."""
+    k: torch.Tensor
+    v: torch.Tensor
+
+    def __post_init__(self):
+        k, v = self.k, self.v
+        _need(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride() and k.stride(3) == 1
+              and k.dtype == v.dtype == torch.bfloat16, "k, v: bf16 [pages, heads, page_size, head_dim], same strides")
+        _need(k.device == v.device, "tensors on one device only")
+
+    def struct(self) -> hq_pages:
+        k = self.k
+        n, h, p, d = k.shape
+        sn, sh, sp, _ = k.stride()
+        return hq_pages(k.data_ptr(), self.v.data_ptr(), n, p, h, d, sn, sh, sp)
+
+
+def alloc_pages(pages: int, page_size: int, heads: int, head_dim: int, device="cuda") -> Pages:
+    """A pool whose page [p, h] is a slab hq_kv_encode takes (page_size rows of head_dim)."""
+    shape = (pages, heads, page_size, head_dim)
+    return Pages(torch.empty(shape, dtype=torch.bfloat16, device=device),
+                 torch.empty(shape, dtype=torch.bfloat16, device=device))
+
+
+def hq_kv_append(k, v, slots, pages: Pages, positions=None, rope: RopeTable | None = None, q=None, q_out=None,
+                 status=None, stream=None):
+    """Write k (rotated at positions if rope is given) and v, [tokens, heads,
+    head_dim] in bf16 or fp32, to slots (int64 [tokens], page * page_size +
+    offset; negative: skipped) of the pool; q is rotated into q_out beside them."""
+    tokens = k.shape[0]
+    _, heads, _, d = pages.k.shape
+    _need(tuple(k.shape) == tuple(v.shape) == (tokens, heads, d), "k, v: [tokens, heads, head_dim] of the pool")
+    _need(slots.dtype == torch.int64 and slots.is_contiguous() and slots.numel() == tokens,
+          "slots: contiguous int64 [tokens]")
+    _need((q is None) == (q_out is None), "q and q_out together")
+    ks, vs, ps = _rows(k, "k"), _rows(v, "v"), pages.struct()
+    qs = os_ = None
+    q_heads = 0
+    if q is not None:
+        _need(q.shape == q_out.shape and q.shape[0] == tokens and q.shape[2] == d, "q, q_out: [tokens, q heads, head_dim]")
+        q_heads = q.shape[1]
+        qs, os_ = ctypes.byref(_rows(q, "q")), ctypes.byref(_rows(q_out, "q_out"))
+    turns, r, layout, amplitude = None, 0, 0, 1.0
+    if rope is not None:
+        _check_rope(positions, rope, tokens)
+        turns, r, layout, amplitude = rope.turns, rope.rotary_dim, rope.layout, rope.amplitude
+    dev = _on_one_device(k, v, slots, pages.k, q, q_out, turns, positions if rope is not None else None, status)
+    _call(_lib.hq_kv_append, dev, stream,
+          (qs, os_, q_heads, ctypes.byref(ks), ctypes.byref(vs), tokens, _ptr(positions) if rope is not None else 0,
+           _ptr(turns), r, layout, amplitude, slots.data_ptr(), ctypes.byref(ps)), (_ptr(status),))
+    return pages
+
+
+def hq_paged_attention_workspace_bytes(batch: int, tokens: int, max_q: int, max_kv: int, heads: int, head_dim: int,
+                                       group: int = 1) -> int:
+    out = _u64(0)
+    _check(_lib.hq_paged_attention_workspace_bytes(batch, tokens, max_q, max_kv, heads, head_dim, group,
+                                                   ctypes.byref(out)), "hq_paged_attention_workspace_bytes")
+    return out.value
+
+
+def alloc_paged_attention_workspace(batch: int, tokens: int, max_q: int, max_kv: int, heads: int, group: int,
+                                    head_dim: int, device="cuda") -> torch.Tensor:
+    """Workspace of hq_paged_attention calls within these bounds (heads: KV heads)."""
+    return torch.empty(max(hq_paged_attention_workspace_bytes(batch, tokens, max_q, max_kv, heads, head_dim, group), 16),
+                       dtype=torch.uint8, device=device)
+
+
+def hq_paged_attention(q, q_start, kv_len, pages: Pages, page_table, scale: float, out, workspace, max_q: int,
+                       max_kv: int, causal: bool = True, window: int = 0, lse=None, status=None, stream=None):
+    """Attention of the new tokens q (bf16 [tokens, heads * group, head_dim];
+    sequence b: rows q_start[b] .. q_start[b + 1]) over kv_len[b] cached tokens
+    of each sequence (the new ones included), found through page_table (int32
+    [batch, pages per sequence]); out bf16 or fp32 like q, lse fp32 [tokens,
+    heads * group]."""
+    tokens, heads, d = q.shape
+    batch = kv_len.numel()
+    _, kvh, _, pd = pages.k.shape
+    _need(out.shape == q.shape and d == pd and heads % kvh == 0, "q, out: [tokens, heads * group, head_dim] of the pool")
+    _need(q_start.dtype == kv_len.dtype == page_table.dtype == torch.int32 and q_start.is_contiguous()
+          and kv_len.is_contiguous() and q_start.numel() == batch + 1,
+          "q_start: int32 [batch + 1], kv_len: int32 [batch], both contiguous")
+    _need(page_table.dim() == 2 and page_table.shape[0] == batch and (page_table.stride(1) == 1 or page_table.numel() == 0
+                                                                      or page_table.shape[1] == 1),
+          "page_table: int32 [batch, pages], contiguous rows")
+    _need(lse is None or (lse.dtype == torch.float32 and lse.is_contiguous() and lse.numel() == tokens * heads),
+          "lse: contiguous fp32 [tokens, heads]")
+    dev = _on_one_device(q, q_start, kv_len, pages.k, page_table, out, workspace, lse, status)
+    qs, os_, ps = _rows(q, "q"), _rows(out, "out"), pages.struct()
+    _call(_lib.hq_paged_attention, dev, stream,
+          (ctypes.byref(qs), q_start.data_ptr(), kv_len.data_ptr(), batch, tokens, max_q, max_kv, heads // kvh,
+           ctypes.byref(ps), page_table.data_ptr(), page_table.shape[1], page_table.stride(0), scale, int(causal),
+           window, ctypes.byref(os_), _ptr(lse), workspace.data_ptr(), workspace.numel()), (_ptr(status),))
+    return out
+
+
+def hq_attention_merge(a, lse_a, b, lse_b, out, lse=None, stream=None):
+    """Join two partial attention results a, b [tokens, heads, head_dim] (bf16 or
+    fp32) by their lse (fp32 [tokens, heads]) into out, which may be a or b."""
+    tokens, heads, d = a.shape
+    _need(b.shape == a.shape and out.shape == a.shape, "a, b, out of one shape")
+    for t in (lse_a, lse_b, lse):
+        _need(t is None or (t.dtype == torch.float32 and t.is_contiguous() and t.numel() == tokens * heads),
+              "lse: contiguous fp32 [tokens, heads]")
+    dev = _on_one_device(a, b, out, lse_a, lse_b, lse)
+    as_, bs, os_ = _rows(a, "a"), _rows(b, "b"), _rows(out, "out")
+    _call(_lib.hq_attention_merge, dev, stream,
+          (ctypes.byref(as_), lse_a.data_ptr(), ctypes.byref(bs), lse_b.data_ptr(), tokens, heads, d, ctypes.byref(os_),
+           _ptr(lse)))
     return out
 
 
