@@ -74,13 +74,13 @@ constexpr size_t few_smem() { return (size_t)16 * WM * D * 2 + (size_t)few_stage
 // Tiles before each sequence, the place where each block's share begins, and
 // cleared counters.  One block; a warp counts a sequence's row tiles.
 template <int T, int RT>
-__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedArgs a, const int report)
+__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedArgs a, const int parts)
 {
     __shared__ int64_t w[kPlanThreads];
     __shared__ int64_t wsum[kPlanThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_launch();
-    for (int c = tid; c < a.grid; c += kPlanThreads) a.counter[c] = 0u;
+    for (int c = tid; c < a.grid * parts; c += kPlanThreads) a.counter[c] = 0u;
     int64_t before = 0;
     for (int b0 = 0; b0 < a.batch; b0 += kPlanThreads) {
         for (int i = warp; i < kPlanThreads; i += kPlanThreads / 32) {
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedArg
             if (b < a.batch) {
                 bool bad;
                 const Seq s = load_seq(a, b, bad);
-                if (bad && report && lane == 0 && a.status) atomicOr(a.status, kStatusIndex);
+                if (bad && lane == 0 && a.status) atomicOr(a.status, kStatusIndex);
                 const int nrt = (s.rows + RT - 1) / RT;
                 for (int rt = lane; rt < nrt; rt += 32) {
                     int t0, n, lo, hi;
@@ -491,8 +491,7 @@ namespace {
 template <int D, int WM>
 cudaError_t launch_few(const PagedArgs &a, cudaStream_t s)
 {
-    paged_plan_kernel<kFewT, 16 * WM><<<1, kPlanThreads, 0, s>>>(a, 1);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_paged_plan(a, kFewT, 16 * WM, 1, s);
     if (e != cudaSuccess) return e;
     constexpr int smem = (int)few_smem<D, WM>();
     e = cudaFuncSetAttribute(paged_few_kernel<D, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -512,40 +511,83 @@ cudaError_t launch_few_d(const PagedArgs &a, int rows, cudaStream_t s)
 
 }  // namespace
 
-// 16, 32 or 64 rows per tile: the fewest that hold the longest sequence's
-// rows.  Blocks: as many as are resident at once (shared memory allows 3, 2 and
-// 1 per SM at head_dim 64, 128 and 256).
+cudaError_t launch_paged_plan(const PagedArgs &a, int T, int RT, int parts, cudaStream_t s)
+{
+    if (T == 128) paged_plan_kernel<128, 256><<<1, kPlanThreads, 0, s>>>(a, parts);
+    else if (RT == 128) paged_plan_kernel<64, 128><<<1, kPlanThreads, 0, s>>>(a, parts);
+    else if (RT == 64) paged_plan_kernel<64, 64><<<1, kPlanThreads, 0, s>>>(a, parts);
+    else if (RT == 32) paged_plan_kernel<64, 32><<<1, kPlanThreads, 0, s>>>(a, parts);
+    else paged_plan_kernel<64, 16><<<1, kPlanThreads, 0, s>>>(a, parts);
+    return cudaGetLastError();
+}
+
+// Which kernel takes which sequences.  Up to 64 rows per sequence (new tokens x
+// group) the mma.sync kernel keeps pace with HBM: 16, 32 or 64 rows per tile,
+// the fewest that hold the longest sequence's rows.  Beyond, the tcgen05
+// kernel; in a batch, sequences of at most 16 rows (tokens being decoded
+// beside a prompt) still go to the other one.  Blocks: as many as are resident
+// at once (shared memory allows 3, 2 and 1 of the mma.sync kernel per SM at
+// head_dim 64, 128 and 256, one of the tcgen05 kernel).
 PagedPlan paged_plan(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_kv, int heads, int group, int head_dim)
 {
     PagedPlan p{};
     const int64_t rows = max_q * group;
-    p.rows_few = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-    p.grid_few = sm_count() * (head_dim == 64 ? 3 : head_dim == 128 ? 2 : 1);
-    auto up = [](uint64_t v) { return (v + 255) / 256 * 256; };
-    p.prefix_bytes = up(8 * (uint64_t)(batch + 1));
-    p.start_bytes = up(sizeof(PagedStart) * (uint64_t)p.grid_few);
-    p.counter_bytes = up(4 * (uint64_t)p.grid_few);
-    p.part_bytes = up(2 * (uint64_t)p.grid_few * p.rows_few * (head_dim + 2) * 4);
-    p.total = p.prefix_bytes + p.start_bytes + p.counter_bytes + p.part_bytes;
+    uint64_t at = 0;
+    auto take = [&](uint64_t bytes) {
+        const uint64_t o = at;
+        at += (bytes + 255) / 256 * 256;
+        return o;
+    };
+    auto place = [&](PagedShare &k, int parts) {
+        k.prefix = take(8 * (uint64_t)(batch + 1));
+        k.start = take(sizeof(PagedStart) * (uint64_t)k.grid);
+        k.counter = take(4 * (uint64_t)k.grid * parts);
+        k.part = take(2 * (uint64_t)k.grid * k.rows * (head_dim + 2) * 4);
+    };
+    const bool many = rows > 64;
+    if (!many || batch > 1) {
+        p.few.rows = many || rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+        p.few.row_hi = many ? 16 : INT32_MAX;
+        p.few.grid = sm_count() * (head_dim == 64 ? 3 : head_dim == 128 ? 2 : 1);
+        place(p.few, 1);
+    }
+    if (many) {
+        p.many.rows = paged_many_rows(head_dim);
+        p.many.row_lo = batch > 1 ? 16 : 0;
+        p.many.row_hi = INT32_MAX;
+        p.many.grid = sm_count();
+        place(p.many, p.many.rows / 128);
+    }
+    p.total = at;
     return p;
 }
 
 cudaError_t launch_paged(const PagedArgs &args, const PagedPlan &p, int head_dim, void *workspace, cudaStream_t s)
 {
-    PagedArgs a = args;
-    char *w = static_cast<char *>(workspace);
-    a.prefix = reinterpret_cast<int64_t *>(w);
-    a.start = reinterpret_cast<PagedStart *>(w + p.prefix_bytes);
-    a.counter = reinterpret_cast<uint32_t *>(w + p.prefix_bytes + p.start_bytes);
-    a.part = reinterpret_cast<float *>(w + p.prefix_bytes + p.start_bytes + p.counter_bytes);
-    a.grid = p.grid_few;
+    auto share = [&](const PagedShare &k) {
+        PagedArgs a = args;
+        char *w = static_cast<char *>(workspace);
+        a.prefix = reinterpret_cast<int64_t *>(w + k.prefix);
+        a.start = reinterpret_cast<PagedStart *>(w + k.start);
+        a.counter = reinterpret_cast<uint32_t *>(w + k.counter);
+        a.part = reinterpret_cast<float *>(w + k.part);
+        a.grid = k.grid;
+        a.row_lo = k.row_lo;
+        a.row_hi = k.row_hi;
+        return a;
+    };
+    if (p.many.grid) {
+        PagedArgs a = share(p.many);
+        a.min_tiles = 4;
+        const cudaError_t e = launch_paged_many(a, head_dim, s);
+        if (e != cudaSuccess || !p.few.grid) return e;
+    }
+    PagedArgs a = share(p.few);
     a.min_tiles = 2;
-    a.row_lo = 0;
-    a.row_hi = INT32_MAX;
     switch (head_dim) {
-    case 64: return launch_few_d<64>(a, p.rows_few, s);
-    case 128: return launch_few_d<128>(a, p.rows_few, s);
-    default: return launch_few_d<256>(a, p.rows_few, s);
+    case 64: return launch_few_d<64>(a, p.few.rows, s);
+    case 128: return launch_few_d<128>(a, p.few.rows, s);
+    default: return launch_few_d<256>(a, p.few.rows, s);
     }
 }
 

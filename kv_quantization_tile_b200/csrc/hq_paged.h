@@ -88,15 +88,25 @@ struct PagedArgs {
     int32_t *status;
 };
 
-// Sizes a launch needs.
+// What a launch of one of the kernels needs of the workspace.
+struct PagedShare {
+    int grid, rows;                // blocks (0: not launched), rows per row tile
+    int row_lo, row_hi;            // the sequences it takes (rows: new tokens x group)
+    uint64_t prefix, start, counter, part;  // offsets
+};
+
 struct PagedPlan {
-    int grid_few, rows_few;     // mma.sync kernel: blocks, rows per row tile
-    int grid_many, rows_many;   // tcgen05 kernel: blocks (0: not launched), rows per row tile
-    uint64_t prefix_bytes, start_bytes, counter_bytes, part_bytes, total;
+    PagedShare few, many;          // mma.sync and tcgen05 kernels
+    uint64_t total;
 };
 
 PagedPlan paged_plan(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_kv, int heads, int group, int head_dim);
 cudaError_t launch_paged(const PagedArgs &a, const PagedPlan &p, int head_dim, void *workspace, cudaStream_t s);
+// The plan kernel for token tiles of T and row tiles of RT, with `parts`
+// counters per block; the tcgen05 kernel with its plan, and its row tile.
+cudaError_t launch_paged_plan(const PagedArgs &a, int T, int RT, int parts, cudaStream_t s);
+cudaError_t launch_paged_many(const PagedArgs &a, int head_dim, cudaStream_t s);
+int paged_many_rows(int head_dim);
 
 #ifdef __CUDACC__
 // ------------------------------------------------------------ device side
