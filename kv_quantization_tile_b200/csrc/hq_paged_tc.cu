@@ -10,21 +10,26 @@
 //   * the product warp issues S = Q K^T (both operands in shared memory) and
 //     O += P V (P in tensor memory, V as it lies, token-major) with
 //     tcgen05.mma; while one MMA tile's softmax runs, the other's products do;
-//   * a warpgroup per MMA tile (its threads one row each, so a row's maximum
-//     and sum need no exchange) reads S from tensor memory, keeps the running
-//     softmax and writes P over S in bf16.
+//   * two warpgroups per MMA tile, a thread of each for every row and each
+//     with half of the tile's tokens, read S from tensor memory, keep the
+//     running softmax and write P over S in bf16.  (With one warpgroup per
+//     MMA tile two warps share a scheduler; alone there, a warp keeps the
+//     exponential unit two thirds busy, and a tile pair took 3350 clocks.)
 // The running maximum is raised, and O rescaled, only where a tile exceeds it
-// by more than 2^8: weights then stay below 2^8, far inside bf16 and binary32,
-// and the final division by their sum cancels the stale maximum exactly
-// ("FlashAttention-4" describes this rule).
+// by more than 24 powers of two: weights then stay below 2^24, sums of 2^30 of
+// them times values up to 2^70 inside binary32, every value keeps its relative
+// precision, and the final division by the weights' sum cancels the stale
+// maximum.  (Rescaling at 8 powers of two, some row of the 256 asked for it in
+// a third of the tiles of a cache with uneven channels, at 1900 clocks each.)
 //
 // Bound: the products are 4 d flops per (row, token), the exponentials one per
 // (row, token) on a unit with 16 per clock and SM: at head_dim 128 a tile pair
-// takes 1024 clocks of tensor pipe and 2048 of exponentials.
+// takes 2048 clocks of tensor pipe and 2048 of exponentials.
 #include <atomic>
 
 #include <cuda.h>
 
+#include "hq_fast.cuh"
 #include "hq_paged.h"
 #include "hq_tcgen05.cuh"
 
@@ -32,14 +37,15 @@ namespace hq {
 
 namespace {
 
-constexpr float kGrow = 8.0f;  // powers of two by which a tile may exceed the running maximum
+constexpr int kPoly = 1;       // of 8 pairs of weights, those computed on the fma pipe
+constexpr float kGrow = 24.0f;  // powers of two by which a tile may exceed the running maximum
 
 template <int D>
 struct Many {
     static constexpr int NT = D == 256 ? 1 : 2;        // MMA tiles of 128 rows
     static constexpr int RT = 128 * NT;
     static constexpr int T = D == 256 ? 64 : 128;      // tokens per tile
-    static constexpr int THREADS = 128 * (NT + 1);
+    static constexpr int THREADS = 256 * NT + 64;
     static constexpr uint32_t TILE = T * D * 2;        // one K or V tile
     static constexpr uint32_t QTILE = 128 * D * 2;
     static constexpr int STAGES = D == 64 ? 8 : 5;
@@ -68,6 +74,18 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d, uint32_t a, uint64_t b,
         : "memory");
 }
 
+// true in one lane of the (converged) warp, the same one every time
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(one));
+    return one;
+}
+
 // 32 consecutive columns of this thread's tensor-memory lane
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32])
 {
@@ -94,6 +112,15 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
           "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
         : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+        :
+        : "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -105,21 +132,6 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes)
 {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
-{
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return done;
-}
-// bounded (mbar_wait); the first poll reads no timer
-__device__ __forceinline__ bool await(uint32_t bar, uint32_t parity) { return mbar_try(bar, parity) || mbar_wait(bar, parity); }
-
 __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap *map, uint32_t bar, int col, int slot, int head, int page)
 {
     asm volatile(
@@ -128,12 +140,72 @@ __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap *map, u
         : "memory");
 }
 
-__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
-
 __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 {
     const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&p);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// 2^x of a pair on the fma pipe, for x <= kGrow and a little over: x = n + f, n
+// its nearest integer (read from the low bits of x + 1.5 2^23), 2^f by a
+// minimax polynomial of degree 5 on [-1/2, 1/2] (relative error 7.5e-8, 2.2e-7
+// in binary32, as ex2.approx's 2^-22), n added to the exponent.  Below 2^-125
+// the result is held there; a NaN stays one.
+__device__ __forceinline__ float2 ex2_poly(float2 x)
+{
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.x) : "f"(-125.0f));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.y) : "f"(-125.0f));
+    const float2 magic = splat2(12582912.0f);
+    const float2 t = add2(x, magic), f = sub2(x, sub2(t, magic));
+    float2 p = fma2(f, splat2(1.3276472454890609e-3f), splat2(9.675540961325169e-3f));
+    p = fma2(p, f, splat2(5.550713092088699e-2f));
+    p = fma2(p, f, splat2(0.24022120237350464f));
+    p = fma2(p, f, splat2(0.6931469440460205f));
+    p = fma2(p, f, splat2(1.0000001192092896f));
+    return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
+                       __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
+}
+
+// Weights of 32 columns of scores: 2^(s scale - off), packed to bf16 pairs,
+// their binary32 sum added to `sum`.  POLY of every 8 pairs go to the fma pipe,
+// the rest to the exponential unit.
+template <int POLY>
+__device__ __forceinline__ void weights32(const uint32_t (&s)[32], float scale, float off, float2 (&sum)[2], uint32_t (&p)[16])
+{
+    const float2 sc = splat2(scale), no = splat2(-off);
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+        const float2 x = fma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sc, no);
+        const float2 y = (i & 7) < POLY ? ex2_poly(x) : make_float2(ex2(x.x), ex2(x.y));
+        sum[i & 1] = add2(sum[i & 1], y);
+        p[i] = pack2(y.x, y.y);
+    }
+}
+
+__device__ __forceinline__ void named_sync(int id, int threads)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// the same, and whether `v` holds for any of the threads
+__device__ __forceinline__ bool named_any(int id, int threads, bool v)
+{
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %3, 0;\n\t"
+        "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}\n"
+        : "=r"(any)
+        : "r"(id), "r"(threads), "r"((uint32_t)v)
+        : "memory");
+    return any;
 }
 
 // byte offset of 16-byte chunk c of row r in a 128-byte-swizzled operand of
@@ -152,10 +224,11 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
     using C = Many<D>;
     constexpr int NT = C::NT, RT = C::RT, T = C::T, STAGES = C::STAGES;
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t s_bar[2 * STAGES + NT * 2 + 4 + 1];
+    __shared__ __align__(8) uint64_t s_bar[2 * STAGES + NT * 2 + 6 + 1];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_fail;
     __shared__ int s_last[NT];
+    __shared__ float s_row[NT][128];  // a value of each row, from one half to the other
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wg = warp >> 2;
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     const uint32_t sq = base, ring = base + NT * C::QTILE;
@@ -166,7 +239,8 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
     auto o_full = [&](int t) { return bar0 + 8u * (uint32_t)(2 * STAGES + NT + t); };
     auto s_full = [&](int b) { return bar0 + 8u * (uint32_t)(2 * STAGES + 2 * NT + b); };
     auto p_full = [&](int b) { return bar0 + 8u * (uint32_t)(2 * STAGES + 2 * NT + 2 + b); };
-    const uint32_t fix_bar = bar0 + 8u * (uint32_t)(2 * STAGES + 2 * NT + 4);
+    auto p_half = [&](int b) { return bar0 + 8u * (uint32_t)(2 * STAGES + 2 * NT + 4 + b); };  // the first 32 weights of either half
+    const uint32_t fix_bar = bar0 + 8u * (uint32_t)(2 * STAGES + 2 * NT + 6);
 
     if (warp == 0) tmem_alloc(smem_u32(&s_tmem), 512);
     if (tid == 0) {
@@ -176,12 +250,13 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
             mbar_init(kv_empty(s), 1);
         }
         for (int t = 0; t < NT; t++) {
-            mbar_init(q_full(t), 4);
+            mbar_init(q_full(t), 8);
             mbar_init(o_full(t), 1);
         }
         for (int b = 0; b < 2; b++) {
             mbar_init(s_full(b), 1);
-            mbar_init(p_full(b), 4);
+            mbar_init(p_full(b), 8);
+            mbar_init(p_half(b), 8);
         }
         mbar_init(fix_bar, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -192,7 +267,7 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
     const uint32_t tmem = s_tmem;
     // a wait that gave up: every role leaves its loops at its next check
     auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-        if (await(bar, parity)) return true;
+        if (mbar_wait(bar, parity)) return true;
         s_fail = 1;
         return false;
     };
@@ -201,19 +276,19 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
     SegWalk<T, RT> w;
     const bool work = w.begin(a);
 
-    if (wg < NT) {
+    if (wg < 2 * NT) {
         // ------------------------------------------------ softmax
-        if constexpr (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        const int t = wg, wl = warp & 3;
+        const int t = wg >> 1, hf = wg & 1, wl = warp & 3;  // MMA tile, half of the tokens, 32 rows
         const uint32_t lanes = (uint32_t)(wl * 32) << 16;
-        const uint32_t to = tmem + lanes + C::O_COL + (uint32_t)(t * D);
+        const uint32_t to = tmem + lanes + C::O_COL + (uint32_t)(t * D + hf * (D / 2));  // this half's columns of O
+        const int pair = 1 + t * 4 + wl;  // barrier of the two warps of the same rows
         uint32_t g = 0;  // tiles so far
         if (work) do {
             const int r0 = w.rt * RT + t * 128;
-            // ---- this warp's 32 query rows
-            constexpr int CH = D / 8;
+            // ---- this warp's half of 32 query rows
+            constexpr int CH = D / 16;
             for (int e = lane; e < 32 * CH; e += 32) {
-                const int rr = wl * 32 + e / CH, c = e % CH, r = r0 + rr;
+                const int rr = wl * 32 + e / CH, c = hf * CH + e % CH, r = r0 + rr;
                 uint4 v = make_uint4(0u, 0u, 0u, 0u);
                 if (r < w.s.rows && a.q_mode != 2) {
                     const int j = (int)fast_div((uint32_t)r, a.group_div), gg = r - j * a.group;
@@ -245,58 +320,87 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                 const int b = NT == 2 ? t : (int)(g & 1u);
                 const uint32_t par = NT == 2 ? g & 1u : (g >> 1) & 1u;
                 const uint32_t ts = tmem + lanes + C::S_COL + (uint32_t)(b * T);
-                ok = wait(s_full(b), par) && !s_fail;
-                if (!__all_sync(FULL, ok)) {
-                    ok = false;
-                    break;
-                }
+                constexpr int NC = T / 64;  // chunks of 32 columns of this half
+                ok = wait(s_full(b), par);
+                // Every product with V is waited for in turn (a barrier's phase can
+                // only be told from the one before it).  With two MMA tiles S comes
+                // after that product anyway; with one, S runs ahead of it.
+                if (NT == 1 && tile > w.first) ok = wait(o_full(t), (g - 1u) & 1u) && ok;
+                ok = __all_sync(FULL, ok);
                 tc_fence_after();
-                uint32_t s[T / 32][32];
+                const uint32_t mine = ts + (uint32_t)(hf * (T / 2));  // this half's scores, then its weights
+                const int tok0 = (w.t0 + tile) * T + hf * (T / 2);
+                const bool edge = !__all_sync(FULL, rlo <= tok0 && rhi >= tok0 + T / 2);
+                auto mask = [&](int c, uint32_t (&s)[32]) {
+                    const int from = rlo - tok0 - 32 * c, to_ = rhi - tok0 - 32 * c;
 #pragma unroll
-                for (int c = 0; c < T / 32; c++) tmem_ld32(ts + 32 * c, s[c]);
-                tmem_wait_ld();
-                const int tok0 = (w.t0 + tile) * T;
-                if (!__all_sync(FULL, rlo <= tok0 && rhi >= tok0 + T)) {
-                    const int from = rlo - tok0, to_ = rhi - tok0;
-#pragma unroll
-                    for (int c = 0; c < T / 32; c++)
-#pragma unroll
-                        for (int i = 0; i < 32; i++)
-                            if (32 * c + i < from || 32 * c + i >= to_) s[c][i] = 0xff800000u;
-                }
+                    for (int i = 0; i < 32; i++)
+                        if (i < from || i >= to_) s[i] = 0xff800000u;
+                };
+                // Weights are rounded to bf16 for the product with V (2^-8 of
+                // each, independent); their sum keeps binary32.  Masked columns
+                // need exact zeros: edge tiles take no polynomial.
+                float2 sum[2] = { make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f) };
+                uint32_t s[32], p[16];
+                auto weights = [&]() {
+                    const float off = m == -INFINITY ? 0.0f : m;  // nothing seen yet: every weight is 0
+                    if (edge) weights32<0>(s, a.scale_log2, off, sum, p);
+                    else weights32<kPoly>(s, a.scale_log2, off, sum, p);
+                };
+                auto hand_over = [&](int c, uint32_t bar) {  // over scores already read
+                    tmem_st16(mine + (uint32_t)(16 * c), p);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar);
+                };
+                // the maximum of the half's scores (its second 32 columns are
+                // read again below, which keeps a thread within 96 registers)
                 float mx[4] = { -INFINITY, -INFINITY, -INFINITY, -INFINITY };
+                auto maxima = [&](const uint32_t (&x)[32]) {
 #pragma unroll
-                for (int c = 0; c < T / 32; c++)
-#pragma unroll
-                    for (int i = 0; i < 32; i++) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[c][i]));
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-                if (tile == w.first) {
-                    m = top;
+                    for (int i = 0; i < 32; i += 2)
+                        mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+                };
+                tmem_ld32(mine, s);
+                if constexpr (NC == 2) {
+                    uint32_t s1[32];
+                    tmem_ld32(mine + 32, s1);
+                    tmem_wait_ld();
+                    if (edge) mask(1, s1);
+                    maxima(s1);
                 } else {
-                    // Every product with V is waited for in turn (a barrier's
-                    // phase can only be told from the one before it).  With two
-                    // MMA tiles S comes after that product anyway; with one, S
-                    // runs ahead of it.
-                    if (NT == 1) {
-                        ok = wait(o_full(t), (g - 1u) & 1u);
-                        if (!__all_sync(FULL, ok)) {
-                            ok = false;
-                            break;
-                        }
+                    tmem_wait_ld();
+                }
+                if (edge) mask(0, s);
+                maxima(s);
+                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+                // The first weights are taken against the running maximum as it
+                // stands, while the other warp gets here, and again in the rare
+                // tile that raises it.
+                weights();
+                if (NC == 2) tmem_ld32(mine + 32, s);
+                if (named_any(pair, 64, tile == w.first || top > m + kGrow || !ok)) {
+                    float *row = &s_row[t][wl * 32 + lane];
+                    if (hf) *row = top;
+                    if (named_any(pair, 64, !ok)) {  // a wait gave up: both warps leave
+                        ok = false;
+                        tmem_wait_ld();
+                        break;
                     }
-                    const bool grow = top > m + kGrow;
-                    if (__any_sync(FULL, grow)) {  // rescale O: the product before this one is complete
-                        const float f = grow ? ex2(m - top) : 1.0f;
-                        if (grow) m = top;
-                        l *= f;
-                        ok = wait(o_full(t), (g - 1u) & 1u);
-                        if (!__all_sync(FULL, ok)) {
-                            ok = false;
-                            break;
-                        }
+                    if (!hf) *row = top = fmaxf(top, *row);
+                    named_sync(pair, 64);
+                    top = *row;
+                    const bool grow = tile == w.first || top > m + kGrow;
+                    const float f = grow && tile > w.first ? ex2(m - top) : 1.0f;
+                    if (grow) m = top;
+                    l *= f;
+                    if (tile > w.first) {  // rescale O: the product before this one is complete
+                        ok = wait(o_full(t), (g - 1u) & 1u);  // (a failure is met at the next vote)
+                        ok = __all_sync(FULL, ok);
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < D / 32; c++) {
+                        for (int c = 0; c < D / 64; c++) {
                             uint32_t o[32];
                             tmem_ld32(to + 32 * c, o);
                             tmem_wait_ld();
@@ -304,41 +408,43 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                             for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
                             tmem_st32(to + 32 * c, o);
                         }
+                        tmem_wait_st();
+                        tc_fence_before();
                     }
+                    named_sync(pair, 64);  // both halves of O are rescaled before either hands P over
+                    tc_fence_after();
+                    tmem_ld32(mine, s);
+                    tmem_wait_ld();
+                    if (edge) mask(0, s);
+                    sum[0] = sum[1] = make_float2(0.0f, 0.0f);
+                    weights();
+                    if (NC == 2) tmem_ld32(mine + 32, s);
                 }
-                const float off = m == -INFINITY ? 0.0f : m;  // nothing seen yet: every weight is 0
-                // weights are rounded to bf16 for the product with V (2^-8 of
-                // each, independent); their sum keeps binary32
-                float sum[4] = { 0.0f, 0.0f, 0.0f, 0.0f };
-#pragma unroll
-                for (int c = 0; c < T / 64; c++) {
-                    uint32_t p[32];
-#pragma unroll
-                    for (int i = 0; i < 32; i++) {
-                        const float x = ex2(fmaf(__uint_as_float(s[2 * c + i / 16][2 * (i & 15)]), a.scale_log2, -off));
-                        const float y = ex2(fmaf(__uint_as_float(s[2 * c + i / 16][2 * (i & 15) + 1]), a.scale_log2, -off));
-                        sum[2 * (i & 1)] += x;
-                        sum[2 * (i & 1) + 1] += y;
-                        p[i] = pack2(x, y);
-                    }
-                    tmem_st32(ts + 32 * c, p);
+                if constexpr (NC == 2) {
+                    tmem_wait_ld();
+                    hand_over(0, p_half(b));
+                    if (edge) mask(1, s);
+                    weights();
+                    hand_over(1, p_full(b));
+                } else {
+                    hand_over(0, p_full(b));
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_full(b));
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }
-            if (!ok) break;
-            // ---- the segment's end
-            ok = wait(o_full(t), (g - 1u) & 1u);
-            if (!__all_sync(FULL, ok)) break;
+            // ---- the segment's end (the MMA tile's warps leave together)
+            ok = ok && wait(o_full(t), (g - 1u) & 1u);
+            if (named_any(9 + t, 256, !ok)) break;
             tc_fence_after();
             const bool whole = w.whole();
             const int rr = wl * 32 + lane;  // row of this MMA tile
+            if (hf) s_row[t][rr] = l;
+            named_sync(pair, 64);
+            if (!hf) s_row[t][rr] = l += s_row[t][rr];
+            named_sync(pair, 64);
+            l = s_row[t][rr];
             // partial results by MMA tile: m and l of its rows, then [D / 4][128] float4
             float *part = a.part + ((int64_t)w.slot() * NT + t) * (128 * (D + 2));
-            if (!whole) {
+            if (!whole && hf == 0) {
                 part[rr] = m;
                 part[128 + rr] = l;
             }
@@ -350,8 +456,8 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                 tok = w.s.q0 + j;
                 head = w.h * a.group + r - j * a.group;
             }
-            const int64_t at = tok * a.out.ts + head * a.out.hs;
-            auto put = [&](int c, const float (&v)[32], float f, bool zero) {  // 32 columns of the row
+            const int64_t at = tok * a.out.ts + head * a.out.hs + hf * (D / 2);
+            auto put = [&](int c, const float (&v)[32], float f, bool zero) {  // 32 of this half's columns of the row
                 if (r >= w.s.rows) return;
                 if (a.out.f32) {
                     float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(a.out.p) + at + 32 * c);
@@ -369,7 +475,7 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                 }
             };
 #pragma unroll 1
-            for (int c = 0; c < D / 32; c++) {
+            for (int c = 0; c < D / 64; c++) {
                 uint32_t o[32];
                 tmem_ld32(to + 32 * c, o);
                 tmem_wait_ld();
@@ -379,7 +485,7 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                     for (int i = 0; i < 32; i++) v[i] = __uint_as_float(o[i]);
                     put(c, v, inv, l == 0.0f);
                 } else {
-                    float4 *p = reinterpret_cast<float4 *>(part + 256) + (8 * c) * 128 + rr;
+                    float4 *p = reinterpret_cast<float4 *>(part + 256) + (hf * (D / 8) + 8 * c) * 128 + rr;
 #pragma unroll
                     for (int i = 0; i < 8; i++)
                         p[i * 128] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
@@ -391,10 +497,10 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
             bool write = whole;
             if (!whole) {
                 __threadfence();
-                group_sync(1 + t);
+                named_sync(9 + t, 256);
                 const int c0 = w.owner(), c1 = w.last();
-                if (wl == 0 && lane == 0) s_last[t] = atomicAdd(a.counter + c0 * NT + t, 1u) == (unsigned)(c1 - c0);
-                group_sync(1 + t);
+                if (hf == 0 && rr == 0) s_last[t] = atomicAdd(a.counter + c0 * NT + t, 1u) == (unsigned)(c1 - c0);
+                named_sync(9 + t, 256);
                 write = s_last[t];
                 if (write) {
                     __threadfence();
@@ -408,13 +514,13 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                     for (int k = c0; k <= c1; k++) lt = fmaf(ex2(__ldcg(part_at(k) + rr) - from), __ldcg(part_at(k) + 128 + rr), lt);
                     const float f = lt == 0.0f ? 0.0f : 1.0f / lt;
 #pragma unroll 1
-                    for (int c = 0; c < D / 32; c++) {
+                    for (int c = 0; c < D / 64; c++) {
                         float v[32];
 #pragma unroll
                         for (int i = 0; i < 32; i++) v[i] = 0.0f;
                         for (int k = c0; k <= c1; k++) {
                             const float e = ex2(__ldcg(part_at(k) + rr) - from);
-                            const float4 *p = reinterpret_cast<const float4 *>(part_at(k) + 256) + (8 * c) * 128 + rr;
+                            const float4 *p = reinterpret_cast<const float4 *>(part_at(k) + 256) + (hf * (D / 8) + 8 * c) * 128 + rr;
 #pragma unroll
                             for (int i = 0; i < 8; i++) {
                                 const float4 x = __ldcg(p + i * 128);
@@ -428,20 +534,25 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                     }
                 }
             }
-            if (write && a.lse && r < w.s.rows)
+            if (write && hf == 0 && a.lse && r < w.s.rows)
                 a.lse[tok * (a.heads * a.group) + head] = lt == 0.0f ? -INFINITY : fmaf(mt, 0.693147180559945309f, logf(lt));
         } while (w.next(a));
     } else {
-        if constexpr (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if ((warp & 3) == 0) {
             // -------------------------------------------- products
-            if (lane == 0 && work) {
+            // The warp walks as one, so addresses stay in uniform registers;
+            // one elected lane issues (always the same one: a commit covers
+            // the products of its own thread).
+            if (work) {
                 constexpr uint32_t ID_S = make_idesc_bf16(128, T);
                 constexpr uint32_t ID_O = make_idesc_bf16(128, D) | (1u << 16);  // V is token-major: B not K-major
+                const bool one = elect_one();
+                const uint64_t qd = swizzled_desc(sq, 16, 1024), kd = swizzled_desc(ring, 16, 1024),
+                               vd = swizzled_desc(ring, T * 128, 1024);
                 uint32_t slot = 0, phase = 0, g = 0, seg = 0;
                 bool ok = true;
                 auto take = [&]() -> uint32_t {  // the next tile of the ring, landed
-                    ok = ok && wait(kv_full(slot), phase) && !s_fail;
+                    ok = ok && wait(kv_full(slot), phase);
                     const uint32_t s = slot;
                     if (++slot == STAGES) {
                         slot = 0;
@@ -449,21 +560,32 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                     }
                     return s;
                 };
-                auto scores = [&](int t, int b, uint32_t s) {
-                    const uint32_t q = sq + t * C::QTILE, k = ring + s * C::TILE, d = tmem + C::S_COL + (uint32_t)(b * T);
-#pragma unroll
-                    for (int i = 0; i < D / 16; i++)
-                        umma_bf16(d, swizzled_desc(q + (i >> 2) * 16384 + (i & 3) * 32, 16, 1024),
-                                  swizzled_desc(k + (i >> 2) * (T * 128) + (i & 3) * 32, 16, 1024), ID_S, i > 0);
-                    umma_commit(s_full(b));
+                auto commit = [&](uint32_t bar) {
+                    if (one) umma_commit(bar);
                 };
-                auto outputs = [&](int t, int b, uint32_t s, bool add) {
-                    const uint32_t p = tmem + C::S_COL + (uint32_t)(b * T), v = ring + s * C::TILE;
+                auto scores = [&](int t, int b, uint32_t s) {
+                    const uint64_t q = qd + (uint32_t)t * (C::QTILE >> 4), k = kd + s * (C::TILE >> 4);
+                    const uint32_t d = tmem + C::S_COL + (uint32_t)(b * T);
+                    if (one) {
 #pragma unroll
-                    for (int i = 0; i < T / 16; i++)
-                        umma_bf16_ts(tmem + C::O_COL + (uint32_t)(t * D), p + 8 * i, swizzled_desc(v + i * 2048, T * 128, 1024), ID_O,
-                                     add || i > 0);
-                    umma_commit(o_full(t));
+                        for (int i = 0; i < D / 16; i++)
+                            umma_bf16(d, q + (i >> 2) * 1024 + (i & 3) * 2, k + (i >> 2) * (T * 8) + (i & 3) * 2, ID_S, i > 0);
+                        umma_commit(s_full(b));
+                    }
+                };
+                // 16-token steps i0, i0 + 1, .. i1 - 1 of either half of the tile; 16
+                // weights fill 8 columns, a half's begin where its scores did
+                auto outputs = [&](int t, int b, uint32_t s, int i0, int i1, bool add, bool last) {
+                    const uint32_t p = tmem + C::S_COL + (uint32_t)(b * T), d = tmem + C::O_COL + (uint32_t)(t * D);
+                    const uint64_t v = vd + s * (C::TILE >> 4);
+                    if (one) {
+#pragma unroll
+                        for (int h = 0; h < 2; h++)
+#pragma unroll
+                            for (int i = i0; i < i1; i++)
+                                umma_bf16_ts(d, p + h * (T / 2) + 8 * i, v + (h * (T / 32) + i) * 128, ID_O, add || h + i > 0);
+                        if (last) umma_commit(o_full(t));
+                    }
                 };
                 do {
                     const uint32_t k0 = take();
@@ -474,39 +596,60 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                         scores(t, NT == 2 ? t : (int)(g & 1u), k0);
                     }
                     if (!ok) break;
-                    umma_commit(kv_empty(k0));
+                    commit(kv_empty(k0));
                     for (int j = 0; j < w.count && ok; j++, g++) {
                         const bool more = j + 1 < w.count;
                         const uint32_t k = more ? take() : 0u;
                         if (NT == 1 && more && ok) {
                             scores(0, (int)((g + 1) & 1u), k);
-                            umma_commit(kv_empty(k));
+                            commit(kv_empty(k));
                         }
                         const uint32_t v = take();
-                        for (int t = 0; t < NT && ok; t++) {
+#pragma unroll
+                        for (int t = 0; t < NT; t++) {
+                            if (!ok) break;
                             const int b = NT == 2 ? t : (int)(g & 1u);
-                            ok = wait(p_full(b), NT == 2 ? g & 1u : (g >> 1) & 1u) && !s_fail;
+                            const uint32_t par = NT == 2 ? g & 1u : (g >> 1) & 1u;
+                            if (T == 128) {  // the first 32 weights of either half
+                                ok = wait(p_half(b), par);
+                                if (!ok) break;
+                                tc_fence_after();
+                                outputs(t, b, v, 0, 2, j > 0, false);
+                            }
+                            ok = wait(p_full(b), par);
                             if (!ok) break;
                             tc_fence_after();
-                            outputs(t, b, v, j > 0);
+                            if (T == 128) outputs(t, b, v, 2, 4, true, true);
+                            else outputs(t, b, v, 0, 2, j > 0, true);
                             if (NT == 2 && more) scores(t, t, k);
                         }
                         if (!ok) break;
-                        umma_commit(kv_empty(v));
-                        if (NT == 2 && more) umma_commit(kv_empty(k));
+                        commit(kv_empty(v));
+                        if (NT == 2 && more) commit(kv_empty(k));
                     }
                     seg++;
                 } while (ok && w.next(a));
             }
-            __syncwarp();
         } else if ((warp & 3) == 1 && work) {
             // -------------------------------------------- loads
             const int page_rows = 1 << a.page_shift, box = page_rows < T ? page_rows : T;
             const int col = lane % (D / 64), pg = lane / (D / 64);
             uint32_t slot = 0, phase = 0, fixes = 0;
             bool ok = true;
-            auto load = [&](int tile, bool is_v) {
-                ok = ok && wait(kv_empty(slot), phase ^ 1u) && !s_fail;
+            // this lane's page of a tile (past the pool, where TMA fills zeros,
+            // for a number outside it); read a tile ahead of its use
+            auto page_of = [&](int tile) -> uint32_t {
+                const int tok = (w.t0 + tile) * T + pg * box;
+                if (tile >= w.first + w.count || pg * box >= T || tok >= w.hi || tok + box <= w.lo) return 0;
+                const uint32_t page = (uint32_t)a.table[(int64_t)w.b * a.table_stride + (tok >> a.page_shift)];
+                if (page >= a.pages) {
+                    if (a.status) atomicOr(a.status, kStatusIndex);
+                    return a.pages;
+                }
+                return page;
+            };
+            auto load = [&](int tile, bool is_v, uint32_t page) {
+                ok = ok && wait(kv_empty(slot), phase ^ 1u);
                 ok = __all_sync(FULL, ok);
                 if (!ok) return;
                 const int tok0 = (w.t0 + tile) * T, tok = tok0 + pg * box;
@@ -515,14 +658,6 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                 const bool fix = is_v && (tok0 < w.lo || tok0 + T > w.hi);
                 const uint32_t bar = fix ? fix_bar : kv_full((int)slot);
                 const bool mine = pg * box < T && tok < w.hi && tok + box > w.lo;
-                uint32_t page = 0;
-                if (mine) {
-                    page = (uint32_t)a.table[(int64_t)w.b * a.table_stride + (tok >> a.page_shift)];
-                    if (page >= a.pages) {
-                        page = a.pages;  // past the pool: TMA fills zeros
-                        if (a.status) atomicOr(a.status, kStatusIndex);
-                    }
-                }
                 const uint32_t n = __popc(__ballot_sync(FULL, mine));
                 if (lane == 0) mbar_expect(bar, n * (uint32_t)box * 128u);
                 __syncwarp();
@@ -548,10 +683,14 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
             };
             do {
                 const int e = w.first + w.count;
-                load(w.first, false);
+                uint32_t here = page_of(w.first), next = page_of(w.first + 1);
+                load(w.first, false, here);
                 for (int tile = w.first; tile < e && ok; tile++) {
-                    if (tile + 1 < e) load(tile + 1, false);
-                    load(tile, true);
+                    const uint32_t after = page_of(tile + 2);
+                    if (tile + 1 < e) load(tile + 1, false, next);
+                    load(tile, true, here);
+                    here = next;
+                    next = after;
                 }
             } while (ok && w.next(a));
             // after a wait that gave up, let the copies in flight land

@@ -89,22 +89,34 @@ __device__ __forceinline__ void mbar_init(uint32_t mbar, uint32_t count)
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(mbar), "r"(count) : "memory");
 }
 
+// Whether phase `parity` of an mbarrier is complete (the hardware may hold the
+// thread for a while before it says no).
+__device__ __forceinline__ bool mbar_try(uint32_t mbar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done)
+        : "r"(mbar), "r"(parity)
+        : "memory");
+    return done;
+}
+
 // Bounded wait for phase `parity` of an mbarrier (2^24 polls or 0.5 s of
-// the global timer, whichever first); false if it gave up.
+// the global timer, whichever first); false if it gave up.  The timer is slow
+// to read (a microsecond), so it is first read after 64 polls.
 __device__ __forceinline__ bool mbar_wait(uint32_t mbar, uint32_t parity)
 {
-    const uint64_t t0 = global_ns();
+    uint64_t t0 = 0;
     for (uint32_t i = 0; i < kSpinLimit; i++) {
-        if ((i & 1023u) == 1023u && global_ns() - t0 > kWaitLimitNs) return false;
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}\n"
-            : "=r"(done)
-            : "r"(mbar), "r"(parity)
-            : "memory");
-        if (done) return true;
+        if (mbar_try(mbar, parity)) return true;
+        if ((i & 63u) == 63u) {
+            const uint64_t now = global_ns();
+            if (t0 == 0) t0 = now;
+            else if (now - t0 > kWaitLimitNs) return false;
+        }
     }
     return false;
 }
