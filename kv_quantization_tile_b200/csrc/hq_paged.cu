@@ -74,12 +74,11 @@ constexpr size_t few_smem() { return (size_t)16 * WM * D * 2 + (size_t)few_stage
 // Tiles before each sequence, the place where each block's share begins, and
 // cleared counters.  One block; a warp counts a sequence's row tiles.
 template <int T, int RT>
-__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedArgs a, const int parts)
+__device__ __forceinline__ void plan_share(const PagedArgs &a, const int parts)
 {
     __shared__ int64_t w[kPlanThreads];
     __shared__ int64_t wsum[kPlanThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    pdl_launch();
     for (int c = tid; c < a.grid * parts; c += kPlanThreads) a.counter[c] = 0u;
     int64_t before = 0;
     for (int b0 = 0; b0 < a.batch; b0 += kPlanThreads) {
@@ -155,6 +154,16 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedArg
         st.tile = (int)rest;
         a.start[c] = st;
     }
+}
+
+// Block 0 plans the first kernel's share, block 1 (if launched) the other's.
+template <int T, int RT, int T2, int RT2>
+__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedArgs a, const int parts, const PagedArgs a2,
+                                                                  const int parts2)
+{
+    pdl_launch();
+    if (blockIdx.x == 0) plan_share<T, RT>(a, parts);
+    else plan_share<T2, RT2>(a2, parts2);
 }
 
 // ------------------------------------------------------------ few rows
@@ -491,10 +500,8 @@ namespace {
 template <int D, int WM>
 cudaError_t launch_few(const PagedArgs &a, cudaStream_t s)
 {
-    cudaError_t e = launch_paged_plan(a, kFewT, 16 * WM, 1, s);
-    if (e != cudaSuccess) return e;
     constexpr int smem = (int)few_smem<D, WM>();
-    e = cudaFuncSetAttribute(paged_few_kernel<D, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(paged_few_kernel<D, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     return launch_dependent(paged_few_kernel<D, WM>, a.grid, kFewThreads, smem, s, a);
 }
@@ -509,17 +516,26 @@ cudaError_t launch_few_d(const PagedArgs &a, int rows, cudaStream_t s)
     }
 }
 
-}  // namespace
-
-cudaError_t launch_paged_plan(const PagedArgs &a, int T, int RT, int parts, cudaStream_t s)
+cudaError_t launch_plan_few(const PagedArgs &a, int rows, cudaStream_t s)
 {
-    if (T == 128) paged_plan_kernel<128, 256><<<1, kPlanThreads, 0, s>>>(a, parts);
-    else if (RT == 128) paged_plan_kernel<64, 128><<<1, kPlanThreads, 0, s>>>(a, parts);
-    else if (RT == 64) paged_plan_kernel<64, 64><<<1, kPlanThreads, 0, s>>>(a, parts);
-    else if (RT == 32) paged_plan_kernel<64, 32><<<1, kPlanThreads, 0, s>>>(a, parts);
-    else paged_plan_kernel<64, 16><<<1, kPlanThreads, 0, s>>>(a, parts);
+    switch (rows) {
+    case 16: paged_plan_kernel<kFewT, 16, kFewT, 16><<<1, kPlanThreads, 0, s>>>(a, 1, a, 1); break;
+    case 32: paged_plan_kernel<kFewT, 32, kFewT, 32><<<1, kPlanThreads, 0, s>>>(a, 1, a, 1); break;
+    default: paged_plan_kernel<kFewT, 64, kFewT, 64><<<1, kPlanThreads, 0, s>>>(a, 1, a, 1); break;
+    }
     return cudaGetLastError();
 }
+
+// the tcgen05 kernel's share, and beside it the mma.sync kernel's of 16 rows per tile
+cudaError_t launch_plan_many(const PagedArgs &many, const PagedArgs &few, int head_dim, bool both, cudaStream_t s)
+{
+    const int rows = paged_many_rows(head_dim);
+    if (rows == 256) paged_plan_kernel<128, 256, kFewT, 16><<<both ? 2 : 1, kPlanThreads, 0, s>>>(many, 2, few, 1);
+    else paged_plan_kernel<64, 128, kFewT, 16><<<both ? 2 : 1, kPlanThreads, 0, s>>>(many, 1, few, 1);
+    return cudaGetLastError();
+}
+
+}  // namespace
 
 // Which kernel takes which sequences.  Up to 64 rows per sequence (new tokens x
 // group) the mma.sync kernel keeps pace with HBM: 16, 32 or 64 rows per tile,
@@ -576,14 +592,19 @@ cudaError_t launch_paged(const PagedArgs &args, const PagedPlan &p, int head_dim
         a.row_hi = k.row_hi;
         return a;
     };
-    if (p.many.grid) {
-        PagedArgs a = share(p.many);
-        a.min_tiles = 4;
-        const cudaError_t e = launch_paged_many(a, head_dim, s);
-        if (e != cudaSuccess || !p.few.grid) return e;
-    }
     PagedArgs a = share(p.few);
     a.min_tiles = 2;
+    cudaError_t e;
+    if (p.many.grid) {
+        PagedArgs b = share(p.many);
+        b.min_tiles = 4;
+        e = launch_plan_many(b, a, head_dim, p.few.grid > 0, s);
+        if (e == cudaSuccess) e = launch_paged_many(b, head_dim, s);
+        if (!p.few.grid) return e;
+    } else {
+        e = launch_plan_few(a, p.few.rows, s);
+    }
+    if (e != cudaSuccess) return e;
     switch (head_dim) {
     case 64: return launch_few_d<64>(a, p.few.rows, s);
     case 128: return launch_few_d<128>(a, p.few.rows, s);

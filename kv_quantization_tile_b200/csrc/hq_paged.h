@@ -102,9 +102,7 @@ struct PagedPlan {
 
 PagedPlan paged_plan(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_kv, int heads, int group, int head_dim);
 cudaError_t launch_paged(const PagedArgs &a, const PagedPlan &p, int head_dim, void *workspace, cudaStream_t s);
-// The plan kernel for token tiles of T and row tiles of RT, with `parts`
-// counters per block; the tcgen05 kernel with its plan, and its row tile.
-cudaError_t launch_paged_plan(const PagedArgs &a, int T, int RT, int parts, cudaStream_t s);
+// The tcgen05 kernel (planned before), and its row tile.
 cudaError_t launch_paged_many(const PagedArgs &a, int head_dim, cudaStream_t s);
 int paged_many_rows(int head_dim);
 

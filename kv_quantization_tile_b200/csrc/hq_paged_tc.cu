@@ -283,34 +283,39 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
         const uint32_t to = tmem + lanes + C::O_COL + (uint32_t)(t * D + hf * (D / 2));  // this half's columns of O
         const int pair = 1 + t * 4 + wl;  // barrier of the two warps of the same rows
         uint32_t g = 0;  // tiles so far
-        if (work) do {
+        // this warp's half of 32 query rows of the segment w stands at
+        auto queries = [&]() {
+            constexpr int CH = D / 16, N = CH;  // chunks per half row, loads per lane
             const int r0 = w.rt * RT + t * 128;
-            // ---- this warp's half of 32 query rows
-            constexpr int CH = D / 16;
-            for (int e = lane; e < 32 * CH; e += 32) {
-                const int rr = wl * 32 + e / CH, c = hf * CH + e % CH, r = r0 + rr;
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            uint4 v[N];
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+                const int e = lane + 32 * i, r = r0 + wl * 32 + e / CH, c = hf * CH + e % CH;
+                v[i] = make_uint4(0u, 0u, 0u, 0u);
                 if (r < w.s.rows && a.q_mode != 2) {
                     const int j = (int)fast_div((uint32_t)r, a.group_div), gg = r - j * a.group;
-                    v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q.p) + (w.s.q0 + j) * a.q.ts +
-                                                         (w.h * a.group + gg) * a.q.hs + 8 * c);
-                    if (a.q_mode == 1) {
-                        v.x ^= 0x80008000u;
-                        v.y ^= 0x80008000u;
-                        v.z ^= 0x80008000u;
-                        v.w ^= 0x80008000u;
-                    }
+                    v[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q.p) + (w.s.q0 + j) * a.q.ts +
+                                                            (w.h * a.group + gg) * a.q.hs + 8 * c);
                 }
-                const uint32_t dst = sq + t * C::QTILE + swizzled_off(128, rr, c);
-                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+            }
+            const uint32_t flip = a.q_mode == 1 ? 0x80008000u : 0u;
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+                const int e = lane + 32 * i;
+                const uint32_t dst = sq + t * C::QTILE + swizzled_off(128, wl * 32 + e / CH, hf * CH + e % CH);
+                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(v[i].x ^ flip), "r"(v[i].y ^ flip),
+                             "r"(v[i].z ^ flip), "r"(v[i].w ^ flip) : "memory");
             }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full(t));
-
-            const int r = r0 + wl * 32 + lane;
+        };
+        bool more = work;
+        if (more) queries();
+        while (more) {
+            const int r = w.rt * RT + t * 128 + wl * 32 + lane, rows = w.s.rows, q0 = w.s.q0, h = w.h;
             int rlo = 0, rhi = 0;
-            if (r < w.s.rows) {
+            if (r < rows) {
                 const int j = (int)fast_div((uint32_t)r, a.group_div);
                 seen_range(a, w.s, j, j, rlo, rhi);
             }
@@ -436,6 +441,11 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
             if (named_any(9 + t, 256, !ok)) break;
             tc_fence_after();
             const bool whole = w.whole();
+            const int slot = w.slot(), c0 = w.owner(), c1 = w.last();
+            // the next segment's queries take the place of this one's, whose
+            // products are done: its first scores come while O is written out
+            more = w.next(a);
+            if (more) queries();
             const int rr = wl * 32 + lane;  // row of this MMA tile
             if (hf) s_row[t][rr] = l;
             named_sync(pair, 64);
@@ -443,7 +453,7 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
             named_sync(pair, 64);
             l = s_row[t][rr];
             // partial results by MMA tile: m and l of its rows, then [D / 4][128] float4
-            float *part = a.part + ((int64_t)w.slot() * NT + t) * (128 * (D + 2));
+            float *part = a.part + ((int64_t)slot * NT + t) * (128 * (D + 2));
             if (!whole && hf == 0) {
                 part[rr] = m;
                 part[128 + rr] = l;
@@ -451,14 +461,14 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             int64_t tok = 0;
             int head = 0;
-            if (r < w.s.rows) {
+            if (r < rows) {
                 const int j = (int)fast_div((uint32_t)r, a.group_div);
-                tok = w.s.q0 + j;
-                head = w.h * a.group + r - j * a.group;
+                tok = q0 + j;
+                head = h * a.group + r - j * a.group;
             }
             const int64_t at = tok * a.out.ts + head * a.out.hs + hf * (D / 2);
             auto put = [&](int c, const float (&v)[32], float f, bool zero) {  // 32 of this half's columns of the row
-                if (r >= w.s.rows) return;
+                if (r >= rows) return;
                 if (a.out.f32) {
                     float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(a.out.p) + at + 32 * c);
 #pragma unroll
@@ -498,7 +508,6 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
             if (!whole) {
                 __threadfence();
                 named_sync(9 + t, 256);
-                const int c0 = w.owner(), c1 = w.last();
                 if (hf == 0 && rr == 0) s_last[t] = atomicAdd(a.counter + c0 * NT + t, 1u) == (unsigned)(c1 - c0);
                 named_sync(9 + t, 256);
                 write = s_last[t];
@@ -518,6 +527,7 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                         float v[32];
 #pragma unroll
                         for (int i = 0; i < 32; i++) v[i] = 0.0f;
+#pragma unroll 2
                         for (int k = c0; k <= c1; k++) {
                             const float e = ex2(__ldcg(part_at(k) + rr) - from);
                             const float4 *p = reinterpret_cast<const float4 *>(part_at(k) + 256) + (hf * (D / 8) + 8 * c) * 128 + rr;
@@ -534,9 +544,9 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                     }
                 }
             }
-            if (write && hf == 0 && a.lse && r < w.s.rows)
+            if (write && hf == 0 && a.lse && r < rows)
                 a.lse[tok * (a.heads * a.group) + head] = lt == 0.0f ? -INFINITY : fmaf(mt, 0.693147180559945309f, logf(lt));
-        } while (w.next(a));
+        }
     } else {
         if ((warp & 3) == 0) {
             // -------------------------------------------- products
@@ -550,7 +560,7 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                 const uint64_t qd = swizzled_desc(sq, 16, 1024), kd = swizzled_desc(ring, 16, 1024),
                                vd = swizzled_desc(ring, T * 128, 1024);
                 uint32_t slot = 0, phase = 0, g = 0, seg = 0;
-                bool ok = true;
+                bool ok = true, again = false;
                 auto take = [&]() -> uint32_t {  // the next tile of the ring, landed
                     ok = ok && wait(kv_full(slot), phase);
                     const uint32_t s = slot;
@@ -597,8 +607,10 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                     }
                     if (!ok) break;
                     commit(kv_empty(k0));
-                    for (int j = 0; j < w.count && ok; j++, g++) {
-                        const bool more = j + 1 < w.count;
+                    const int count = w.count;
+                    again = w.next(a);  // (its lengths are read while the first softmax runs)
+                    for (int j = 0; j < count && ok; j++, g++) {
+                        const bool more = j + 1 < count;
                         const uint32_t k = more ? take() : 0u;
                         if (NT == 1 && more && ok) {
                             scores(0, (int)((g + 1) & 1u), k);
@@ -628,7 +640,7 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                         if (NT == 2 && more) commit(kv_empty(k));
                     }
                     seg++;
-                } while (ok && w.next(a));
+                } while (ok && again);
             }
         } else if ((warp & 3) == 1 && work) {
             // -------------------------------------------- loads
@@ -754,7 +766,6 @@ cudaError_t launch_many_d(const PagedArgs &a, cudaStream_t s)
     if (e == cudaSuccess) e = page_map(&vmap, a, a.v, D, box);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(paged_many_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
-    if (e == cudaSuccess) e = launch_paged_plan(a, C::T, C::RT, C::NT, s);
     if (e != cudaSuccess) return e;
     return launch_dependent(paged_many_kernel<D>, a.grid, C::THREADS, C::SMEM, s, a, kmap, vmap);
 }
