@@ -1,9 +1,12 @@
-"""Build the sm_100a codec library (``libhq.so``) in-tree with nvcc.
+"""Build the sm_100a codec library (``libhq.so``) in-tree with nvcc, and the
+extension through which Python calls the serving operators (``_hq_torch.so``)
+with g++.
 
 Each ``csrc/*.cu`` file is compiled to an object in parallel, then linked
 into ``kv_quantization_tile_b200/libhq.so`` with the CUDA runtime linked
-statically.  The build is skipped when the library is newer than every
-source and header.
+statically; ``csrc/hq_torch.cpp`` is compiled against torch's headers and linked
+to that library.  The build is skipped when both are newer than every source
+and header.
 """
 from __future__ import annotations
 
@@ -11,6 +14,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +22,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libhq.so")
+EXT = os.path.join(PKG, "_hq_torch.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
@@ -29,14 +34,14 @@ def _sources():
 
 
 def _deps():
-    return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
+    return (_sources() + [os.path.join(CSRC, "hq_torch.cpp")] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
             + glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)])
 
 
 def stale() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(EXT)):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
@@ -51,6 +56,31 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
+def _run(cmd: list[str], what: str):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def _compile_ext() -> str:
+    import torch
+    from torch.utils import cpp_extension
+    obj = os.path.join(OBJ, "hq_torch.o")
+    inc = [*cpp_extension.include_paths(), os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
+           sysconfig.get_paths()["include"]]
+    _run(["g++", "-O2", "-fPIC", "-std=c++17", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          *[f"-isystem{p}" for p in inc], "-c", os.path.join(CSRC, "hq_torch.cpp"), "-o", obj], "g++ for hq_torch.cpp")
+    return obj
+
+
+def _link_ext(obj: str):
+    from torch.utils import cpp_extension
+    tmp = EXT + f".tmp{os.getpid()}"
+    _run(["g++", "-shared", "-o", tmp, obj, LIB, *[f"-L{p}" for p in cpp_extension.library_paths()], "-lc10", "-lc10_cuda",
+          "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], "link of _hq_torch.so")
+    os.replace(tmp, EXT)
+
+
 def build(force: bool = False, ptxas_verbose: bool = False) -> str:
     """Compile (if stale) and return the path of libhq.so."""
     if not force and not stale():
@@ -58,14 +88,14 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
     os.makedirs(OBJ, exist_ok=True)
     extra = ["-Xptxas", "-v"] if ptxas_verbose else []
     srcs = _sources()
-    with ThreadPoolExecutor(max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with ThreadPoolExecutor(max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        ext = ex.submit(_compile_ext)
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [NVCC, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
+    cmd = [NVCC, *ARCH, "-shared", "-cudart", "static", "-Xlinker", "-soname=libhq.so", "-o", tmp, *objs]
+    _run(cmd, "nvcc link")
     os.replace(tmp, LIB)
+    _link_ext(ext.result())
     return LIB
 
 

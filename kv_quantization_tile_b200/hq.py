@@ -20,6 +20,7 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libhq.so")
 if not os.path.exists(_LIB_PATH):
     raise ImportError(f"{_LIB_PATH} is missing: build it with "
                       "`python -c 'import __graft_entry__ as g; g.build()'`")
+from . import _hq_torch  # noqa: E402  (the serving operators' calls; built beside libhq.so)
 
 HQ_Z, HQ_A2, HQ_D4, HQ_E8 = 1, 2, 4, 8
 HQ_BF16, HQ_F32 = 0, 1
@@ -143,6 +144,9 @@ class HQError(RuntimeError):
     def __init__(self, code: int, where: str):
         super().__init__(f"{where}: {hq_error_string(code)} (code {code})")
         self.code = code
+
+
+_hq_torch.set_error(HQError)
 
 
 def library():
@@ -524,25 +528,9 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _on_one_device(*tensors) -> torch.device:
-    """The CUDA device all given tensors (None skipped) lie on."""
-    dev = tensors[0].device
-    _need(dev.type == "cuda", "CUDA tensors only")
-    for t in tensors:
-        _need(t is None or t.device == dev, "tensors on one device only")
-    return dev
-
-
-def _call(fn, dev: torch.device, stream, args, tail=()):
-    """Run fn(*args, stream handle, *tail) with dev current (its context owns the stream)."""
-    with torch.cuda.device(dev):
-        code = fn(*args, _stream_handle(stream), *tail)
-    _check(code, fn.__name__)
-
-
-def _rows(t: torch.Tensor, what: str) -> hq_rows:
-    _need(t.dim() == 3 and (t.stride(2) == 1 or t.numel() == 0), f"{what}: [tokens, heads, head_dim], last stride 1")
-    return hq_rows(t.data_ptr(), _dtype_code(t), t.stride(0), t.stride(1))
+def _handle(stream):
+    """None (the tensors' device's current stream) or a stream's handle."""
+    return None if stream is None else stream.cuda_stream
 
 
 @dataclass
@@ -588,24 +576,10 @@ def rope_table(rotary_dim: int, base: float = 10000.0, scaling: dict | None = No
     return RopeTable(turns, rotary_dim, ROPE_LAYOUTS[layout], amplitude)
 
 
-def _check_rope(positions, rope: RopeTable, tokens: int):
-    _need(positions is not None and positions.dtype == torch.int64 and positions.is_contiguous()
-          and positions.numel() == tokens, "positions: contiguous int64 [tokens]")
-    _need(rope.turns.dtype == torch.int64 and rope.turns.is_contiguous()
-          and rope.turns.numel() == rope.rotary_dim // 2, "rope.turns: contiguous int64 [rotary_dim / 2]")
-
-
 def hq_rope(x, positions, rope: RopeTable, y, inverse: bool = False, stream=None):
     """Rotate x [tokens, heads, head_dim] (bf16 or fp32, any row strides) at
     positions (int64 [tokens]) into y (which may be x); inverse turns back."""
-    tokens, heads, d = x.shape
-    _need(y.shape == x.shape, "y: the shape of x")
-    _check_rope(positions, rope, tokens)
-    dev = _on_one_device(x, y, positions, rope.turns)
-    xs, ys = _rows(x, "x"), _rows(y, "y")
-    _call(_lib.hq_rope, dev, stream, (ctypes.byref(xs), ctypes.byref(ys), tokens, heads, d, positions.data_ptr(),
-                                      rope.turns.data_ptr(), rope.rotary_dim, rope.layout, rope.amplitude,
-                                      int(inverse)))
+    _hq_torch.rope(x, positions, rope.turns, rope.rotary_dim, rope.layout, rope.amplitude, y, inverse, _handle(stream))
     return y
 
 
@@ -620,13 +594,6 @@ class Pages:
         k, v = self.k, self.v
         _need(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride() and k.stride(3) == 1
               and k.dtype == v.dtype == torch.bfloat16, "k, v: bf16 [pages, heads, page_size, head_dim], same strides")
-        _need(k.device == v.device, "tensors on one device only")
-
-    def struct(self) -> hq_pages:
-        k = self.k
-        n, h, p, d = k.shape
-        sn, sh, sp, _ = k.stride()
-        return hq_pages(k.data_ptr(), self.v.data_ptr(), n, p, h, d, sn, sh, sp)
 
 
 def alloc_pages(pages: int, page_size: int, heads: int, head_dim: int, device="cuda") -> Pages:
@@ -641,27 +608,11 @@ def hq_kv_append(k, v, slots, pages: Pages, positions=None, rope: RopeTable | No
     """Write k (rotated at positions if rope is given) and v, [tokens, heads,
     head_dim] in bf16 or fp32, to slots (int64 [tokens], page * page_size +
     offset; negative: skipped) of the pool; q is rotated into q_out beside them."""
-    tokens = k.shape[0]
-    _, heads, _, d = pages.k.shape
-    _need(tuple(k.shape) == tuple(v.shape) == (tokens, heads, d), "k, v: [tokens, heads, head_dim] of the pool")
-    _need(slots.dtype == torch.int64 and slots.is_contiguous() and slots.numel() == tokens,
-          "slots: contiguous int64 [tokens]")
-    _need((q is None) == (q_out is None), "q and q_out together")
-    ks, vs, ps = _rows(k, "k"), _rows(v, "v"), pages.struct()
-    qs = os_ = None
-    q_heads = 0
-    if q is not None:
-        _need(q.shape == q_out.shape and q.shape[0] == tokens and q.shape[2] == d, "q, q_out: [tokens, q heads, head_dim]")
-        q_heads = q.shape[1]
-        qs, os_ = ctypes.byref(_rows(q, "q")), ctypes.byref(_rows(q_out, "q_out"))
-    turns, r, layout, amplitude = None, 0, 0, 1.0
-    if rope is not None:
-        _check_rope(positions, rope, tokens)
-        turns, r, layout, amplitude = rope.turns, rope.rotary_dim, rope.layout, rope.amplitude
-    dev = _on_one_device(k, v, slots, pages.k, q, q_out, turns, positions if rope is not None else None, status)
-    _call(_lib.hq_kv_append, dev, stream,
-          (qs, os_, q_heads, ctypes.byref(ks), ctypes.byref(vs), tokens, _ptr(positions) if rope is not None else 0,
-           _ptr(turns), r, layout, amplitude, slots.data_ptr(), ctypes.byref(ps)), (_ptr(status),))
+    if rope is None:
+        _hq_torch.append(k, v, slots, pages.k, pages.v, None, None, 0, 0, 1.0, q, q_out, status, _handle(stream))
+    else:
+        _hq_torch.append(k, v, slots, pages.k, pages.v, positions, rope.turns, rope.rotary_dim, rope.layout,
+                         rope.amplitude, q, q_out, status, _handle(stream))
     return pages
 
 
@@ -687,40 +638,15 @@ def hq_paged_attention(q, q_start, kv_len, pages: Pages, page_table, scale: floa
     of each sequence (the new ones included), found through page_table (int32
     [batch, pages per sequence]); out bf16 or fp32 like q, lse fp32 [tokens,
     heads * group]."""
-    tokens, heads, d = q.shape
-    batch = kv_len.numel()
-    _, kvh, _, pd = pages.k.shape
-    _need(out.shape == q.shape and d == pd and heads % kvh == 0, "q, out: [tokens, heads * group, head_dim] of the pool")
-    _need(q_start.dtype == kv_len.dtype == page_table.dtype == torch.int32 and q_start.is_contiguous()
-          and kv_len.is_contiguous() and q_start.numel() == batch + 1,
-          "q_start: int32 [batch + 1], kv_len: int32 [batch], both contiguous")
-    _need(page_table.dim() == 2 and page_table.shape[0] == batch and (page_table.stride(1) == 1 or page_table.numel() == 0
-                                                                      or page_table.shape[1] == 1),
-          "page_table: int32 [batch, pages], contiguous rows")
-    _need(lse is None or (lse.dtype == torch.float32 and lse.is_contiguous() and lse.numel() == tokens * heads),
-          "lse: contiguous fp32 [tokens, heads]")
-    dev = _on_one_device(q, q_start, kv_len, pages.k, page_table, out, workspace, lse, status)
-    qs, os_, ps = _rows(q, "q"), _rows(out, "out"), pages.struct()
-    _call(_lib.hq_paged_attention, dev, stream,
-          (ctypes.byref(qs), q_start.data_ptr(), kv_len.data_ptr(), batch, tokens, max_q, max_kv, heads // kvh,
-           ctypes.byref(ps), page_table.data_ptr(), page_table.shape[1], page_table.stride(0), scale, int(causal),
-           window, ctypes.byref(os_), _ptr(lse), workspace.data_ptr(), workspace.numel()), (_ptr(status),))
+    _hq_torch.attention(q, q_start, kv_len, pages.k, pages.v, page_table, scale, out, workspace, max_q, max_kv, causal,
+                        window, lse, status, _handle(stream))
     return out
 
 
 def hq_attention_merge(a, lse_a, b, lse_b, out, lse=None, stream=None):
     """Join two partial attention results a, b [tokens, heads, head_dim] (bf16 or
     fp32) by their lse (fp32 [tokens, heads]) into out, which may be a or b."""
-    tokens, heads, d = a.shape
-    _need(b.shape == a.shape and out.shape == a.shape, "a, b, out of one shape")
-    for t in (lse_a, lse_b, lse):
-        _need(t is None or (t.dtype == torch.float32 and t.is_contiguous() and t.numel() == tokens * heads),
-              "lse: contiguous fp32 [tokens, heads]")
-    dev = _on_one_device(a, b, out, lse_a, lse_b, lse)
-    as_, bs, os_ = _rows(a, "a"), _rows(b, "b"), _rows(out, "out")
-    _call(_lib.hq_attention_merge, dev, stream,
-          (ctypes.byref(as_), lse_a.data_ptr(), ctypes.byref(bs), lse_b.data_ptr(), tokens, heads, d, ctypes.byref(os_),
-           _ptr(lse)))
+    _hq_torch.merge(a, lse_a, b, lse_b, out, lse, _handle(stream))
     return out
 
 
