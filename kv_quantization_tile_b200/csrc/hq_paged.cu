@@ -12,26 +12,16 @@
 // unnormalised output), and the last block to finish it -- found with a
 // counter, no waiting -- adds them in block order, so results do not depend on
 // which block that was.
-#include "hq_paged.h"
+#include "hq_paged_tma.cuh"
 
 namespace hq {
 
 namespace {
 
-constexpr int kFewThreads = 128, kFewT = 64;
+constexpr int kFewWarps = 4, kFewRows = 32 * kFewWarps;    // consumer warps and their threads
+constexpr int kFewThreads = kFewRows + 32, kFewT = 64;      // and one warp that loads
 constexpr int kPlanThreads = 1024;
-
-__device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
-// 16 bytes global -> shared; nothing is read where !valid (zeros are stored)
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool valid)
-{
-    const int n = valid ? 16 : 0;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+constexpr int kClusterTiles = 16;  // most tiles a block takes of an uneven batch without a plan
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4])
 {
@@ -51,22 +41,16 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack2(float lo, float hi)
-{
-    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&p);
-}
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kFewRows) : "memory"); }
 
-// byte offset of 16-byte chunk c of row r in a [rows][D] bf16 tile; chunks
-// are swizzled by row so that 8 consecutive rows meet 8 bank groups
-template <int D>
-__device__ __forceinline__ uint32_t tile_off(int r, int c) { return (uint32_t)(r * D * 2 + ((c ^ (r & 7)) << 4)); }
-
-// bf16 stages of K and V tiles: about 64 KB in flight per SM keep HBM busy
+// stages of K and V tiles: about 64 KB in flight per SM keep HBM busy
 template <int D>
 constexpr int few_stages() { return D == 64 ? 4 : 3; }
+// blocks per SM that shared memory and registers allow
+template <int D>
+constexpr int few_blocks() { return D == 64 ? 3 : D == 128 ? 2 : 1; }
 template <int D, int WM>
-constexpr size_t few_smem() { return (size_t)16 * WM * D * 2 + (size_t)few_stages<D>() * 2 * kFewT * D * 2; }
+constexpr size_t few_smem() { return 1024 + (D == 256 ? 16 * WM * D * 2 : 0) + (size_t)few_stages<D>() * 2 * kFewT * D * 2; }
 
 }  // namespace
 
@@ -167,93 +151,137 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedArg
 }
 
 // ------------------------------------------------------------ few rows
-// Four warps; a row tile has 16 WM rows.  Warp (wm, wn) multiplies rows
+// Four consumer warps; a row tile has 16 WM rows.  Warp (wm, wn) multiplies rows
 // 16 wm .. with its share of each tile's tokens and keeps its own running
-// softmax; the 4 / WM warps of the same rows are joined after the last tile.
-template <int D, int WM>
-__global__ void __launch_bounds__(kFewThreads) paged_few_kernel(const PagedArgs a)
+// softmax; the 4 / WM warps of the same rows are joined after the last tile.  A
+// fifth warp copies the tiles' pages with TMA into a ring of stages, so the
+// consumers meet no one else between tiles: each waits for a stage's bytes and
+// reports when it has read them.  (With the tiles copied by the consumers
+// themselves, 16 bytes a thread, and a block barrier per tile, a tile took 2500
+// clocks, most of them addresses and waiting.)
+// CLUSTER: no plan; the blocks of a cluster share one job, and join their
+// results through each other's shared memory.
+template <int D, int WM, bool CLUSTER>
+__global__ void __launch_bounds__(kFewThreads, few_blocks<D>())
+paged_few_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
 {
     constexpr int T = kFewT, RT = 16 * WM, WN = 4 / WM, NC = T / WN / 16;  // NC: 16-token chunks per warp and tile
-    constexpr int STAGES = few_stages<D>(), CH = D / 8, KS = D / 16;
+    constexpr int STAGES = few_stages<D>(), KS = D / 16;
     constexpr uint32_t TILE = T * D * 2;
     constexpr bool QREG = D <= 128;  // q fragments stay in registers
-    extern __shared__ __align__(128) uint8_t sm[];
-    uint8_t *sq = sm, *ring = sm + RT * D * 2;
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t s_bar[2 * STAGES];
     __shared__ float s_m[4][16], s_l[4][16];
+    __shared__ float s_fm[CLUSTER ? RT : 1], s_fl[CLUSTER ? RT : 1];
     __shared__ int s_last;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int wm = warp / WN, wn = warp % WN;
-
-    pdl_wait();
+    uint8_t *ring = raw + (((smem_u32(raw) + 1023u) & ~1023u) - smem_u32(raw)), *sq = ring + STAGES * 2 * TILE;
+    const uint32_t bar0 = smem_u32(s_bar), ring0 = smem_u32(ring), sq0 = smem_u32(sq);
+    auto full = [&](uint32_t s) { return bar0 + 8u * s; };
+    auto empty = [&](uint32_t s) { return bar0 + 8u * (STAGES + s); };
+    if (tid == 0) {
+        for (int s = 0; s < STAGES; s++) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), kFewWarps);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
     SegWalk<T, RT> w;
-    if (!w.begin(a)) return;
+    bool work;
+    if constexpr (CLUSTER) {
+        work = w.begin_cluster(a);
+    } else {
+        pdl_wait();
+        work = w.begin(a);
+    }
+    if (!work) return;
+    __syncthreads();
+    uint32_t stage = 0, phase = 0;
+    bool ok = true;  // a wait that gave up ends the loops; results are invalid then
+    auto advance = [&]() {
+        if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    };
     do {
         const int r0 = w.rt * RT, nr = min(RT, w.s.rows - r0);
-        const int32_t *table = a.table + (int64_t)w.b * a.table_stride;
-
-        // ---- queries (rows past the last are zero)
-        for (int e = tid; e < RT * CH; e += kFewThreads) {
-            const int r = e / CH, c = e % CH;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (r < nr && a.q_mode != 2) {
-                const int j = (int)fast_div((uint32_t)(r0 + r), a.group_div), g = r0 + r - j * a.group;
-                v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q.p) + (w.s.q0 + j) * a.q.ts +
-                                                     (w.h * a.group + g) * a.q.hs + 8 * c);
-                if (a.q_mode == 1) {
-                    v.x ^= 0x80008000u;
-                    v.y ^= 0x80008000u;
-                    v.z ^= 0x80008000u;
-                    v.w ^= 0x80008000u;
+        const int end = w.first + w.count;
+        if (warp == kFewWarps) {
+            // -------------------------------------------- loads
+            const int page_rows = 1 << a.page_shift, box = page_rows < T ? page_rows : T;
+            const int col = lane % (D / 64), pg = lane / (D / 64);
+            // this lane's page of a tile (past the pool, where TMA fills zeros,
+            // for a number outside it); read a tile ahead of its use
+            auto page_of = [&](int tile) -> uint32_t {
+                const int tok = (w.t0 + tile) * T + pg * box;
+                if (tile >= end || pg * box >= T || tok >= w.hi || tok + box <= w.lo) return 0;
+                const uint32_t page = (uint32_t)a.table[(int64_t)w.b * a.table_stride + (tok >> a.page_shift)];
+                if (page >= a.pages) {
+                    if (a.status) atomicOr(a.status, kStatusIndex);
+                    return a.pages;
                 }
-            }
-            *reinterpret_cast<uint4 *>(sq + tile_off<D>(r, c)) = v;
-        }
-
-        // ---- K and V tiles into the ring: thread (row, chunk); a page's rows
-        // lie anywhere, tokens outside the job's range are zeros
-        const uint16_t *kb = a.k + w.h * a.head_stride, *vb = a.v + w.h * a.head_stride;
-        const int lr = tid / CH, lc = tid % CH;
-        constexpr int RSTEP = kFewThreads / CH;
-        const int pmask = (1 << a.page_shift) - 1;
-        const int ppt = T >> a.page_shift;  // pages per tile (0: a page holds several tiles)
-        auto page_of = [&](int tile) -> int {  // lane l: l-th page of the tile
-            const int tok = (w.t0 + tile) * T + (lane << a.page_shift);
-            if (tile >= w.first + w.count || lane >= (ppt > 0 ? ppt : 1) || tok >= w.hi) return 0;
-            if (tok + (1 << a.page_shift) <= w.lo) return 0;  // behind the window: its entry may be stale
-            const int p = table[tok >> a.page_shift];
-            if ((uint32_t)p >= a.pages && a.status) atomicOr(a.status, kStatusIndex);
-            return p;
-        };
-        int next_page = page_of(w.first);
-        auto load = [&](int tile) {
-            if (tile < w.first + w.count) {
-                const int stage = (tile - w.first) % STAGES;
-                const uint32_t dk = smem_u32(ring + stage * 2 * TILE), dv = dk + TILE;
-                const int tok0 = (w.t0 + tile) * T;
-#pragma unroll
-                for (int i = 0; i < T / RSTEP; i++) {
-                    const int r = lr + i * RSTEP, tok = tok0 + r;
-                    const int page = __shfl_sync(FULL, next_page, r >> a.page_shift);
-                    const bool ok = tok >= w.lo && tok < w.hi && (uint32_t)page < a.pages;
-                    const int64_t off = ok ? page * a.page_stride + (tok & pmask) * a.slot_stride + 8 * lc : 0;
-                    cp16(dk + tile_off<D>(r, lc), kb + off, ok);
-                    cp16(dv + tile_off<D>(r, lc), vb + off, ok);
+                return page;
+            };
+            uint32_t page = page_of(w.first);
+            for (int tile = w.first; tile < end && ok; tile++) {
+                const uint32_t next = page_of(tile + 1);
+                ok = __all_sync(FULL, mbar_wait(empty(stage), phase ^ 1u));
+                if (!ok) break;
+                const int tok = (w.t0 + tile) * T + pg * box;
+                const bool mine = pg * box < T && tok < w.hi && tok + box > w.lo;
+                const uint32_t n = __popc(__ballot_sync(FULL, mine));
+                if (lane == 0) mbar_expect(full(stage), n * (uint32_t)box * 256u);
+                __syncwarp();
+                if (mine) {
+                    const uint32_t dst = ring0 + stage * 2 * TILE + (uint32_t)(col * T * 128 + pg * box * 128);
+                    const int at = tok & (page_rows - 1);
+                    tma_page(dst, &kmap, full(stage), col * 64, at, w.h, (int)page);
+                    tma_page(dst + TILE, &vmap, full(stage), col * 64, at, w.h, (int)page);
                 }
-                next_page = page_of(tile + 1);
+                page = next;
+                advance();
             }
-            cp_commit();
+            if (!ok)  // let the copies in flight land
+                for (uint32_t s = 0; s < STAGES; s++) mbar_wait(full(s), s < stage ? phase : phase ^ 1u);
+            __syncthreads();  // (A) the ring holds the consumers' outputs until (B)
+            if constexpr (!CLUSTER) ok = !__syncthreads_or(!ok);
+        } else {
+        // ------------------------------------------------ consumers
+        // ---- queries (rows past the last are zero): fragments straight into
+        // registers, or a tile in shared memory (head_dim 256, whose outputs
+        // leave no registers for them)
+        const uint32_t flip = a.q_mode == 1 ? 0x80008000u : 0u;
+        auto query = [&](int r) -> const uint16_t * {  // row r of the tile, null past the last
+            if (r >= nr || a.q_mode == 2) return nullptr;
+            const int j = (int)fast_div((uint32_t)(r0 + r), a.group_div), g = r0 + r - j * a.group;
+            return static_cast<const uint16_t *>(a.q.p) + (w.s.q0 + j) * a.q.ts + (w.h * a.group + g) * a.q.hs;
         };
-#pragma unroll
-        for (int i = 0; i < STAGES - 1; i++) load(w.first + i);
-        __syncthreads();
-
         uint32_t qf[QREG ? KS : 1][4];
         const int arow = 16 * wm + (lane & 15), ach = lane >> 4;
         if constexpr (QREG) {
+            const uint16_t *q[2] = { query(16 * wm + (lane >> 2)), query(16 * wm + (lane >> 2) + 8) };
 #pragma unroll
-            for (int k = 0; k < KS; k++) ldsm4(smem_u32(sq) + tile_off<D>(arow, 2 * k + ach), qf[k]);
+            for (int k = 0; k < KS; k++)
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    qf[k][i] = q[i & 1] ? *reinterpret_cast<const uint32_t *>(q[i & 1] + 16 * k + 8 * (i >> 1) + 2 * (lane & 3)) ^ flip : 0u;
+        } else {
+            for (int e = tid; e < RT * (D / 8); e += kFewRows) {
+                const int r = e / (D / 8), c = e % (D / 8);
+                const uint16_t *q = query(r);
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (q) {
+                    v = *reinterpret_cast<const uint4 *>(q + 8 * c);
+                    v = make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
+                }
+                *reinterpret_cast<uint4 *>(sq + swizzled_off(RT, r, c)) = v;
+            }
+            consumers_sync();
         }
-        // the tokens each of this thread's two rows sees
+        // the tokens each of this thread's two rows sees, and those all of the
+        // warp's rows see
         int rlo[2], rhi[2];
 #pragma unroll
         for (int i = 0; i < 2; i++) {
@@ -264,44 +292,52 @@ __global__ void __launch_bounds__(kFewThreads) paged_few_kernel(const PagedArgs 
                 seen_range(a, w.s, j, j, rlo[i], rhi[i]);
             }
         }
+        // rows past the last compute what nobody reads
+        int all_lo = rlo[0], all_hi = rhi[0];
+        {
+            const int r = 16 * wm + (lane >> 2);
+            if (r >= nr) all_lo = 0, all_hi = INT32_MAX;
+            if (r + 8 < nr) {
+                all_lo = max(all_lo, rlo[1]);
+                all_hi = min(all_hi, rhi[1]);
+            }
+            all_lo = __reduce_max_sync(FULL, all_lo);
+            all_hi = __reduce_min_sync(FULL, all_hi);
+        }
         float o[D / 8][4], m[2] = { -INFINITY, -INFINITY }, l[2] = { 0.0f, 0.0f };
 #pragma unroll
         for (int i = 0; i < D / 8; i++)
 #pragma unroll
             for (int k = 0; k < 4; k++) o[i][k] = 0.0f;
 
-        for (int tile = w.first; tile < w.first + w.count; tile++) {
-            cp_wait<STAGES - 2>();
-            __syncthreads();  // the tile has landed for all; the stage before it is free
-            load(tile + STAGES - 1);
-            const uint32_t sk = smem_u32(ring + ((tile - w.first) % STAGES) * 2 * TILE), sv = sk + TILE;
+        for (int tile = w.first; tile < end; tile++) {
+            ok = __all_sync(FULL, mbar_wait(full(stage), phase));
+            if (!ok) break;
+            const uint32_t sk = ring0 + stage * 2 * TILE, sv = sk + TILE;
             const int tok0 = (w.t0 + tile) * T + wn * (NC * 16);
-            float s[NC][2][4];
+            // two chains per chunk of 16 tokens shorten the wait on the sums
+            float s[NC][2][2][4];
 #pragma unroll
             for (int c = 0; c < NC; c++)
 #pragma unroll
                 for (int n = 0; n < 2; n++)
 #pragma unroll
-                    for (int k = 0; k < 4; k++) s[c][n][k] = 0.0f;
+                    for (int k = 0; k < 4; k++) s[c][n][0][k] = s[c][n][1][k] = 0.0f;
 #pragma unroll
             for (int k = 0; k < KS; k++) {
                 uint32_t qk[4];
-                if constexpr (!QREG) ldsm4(smem_u32(sq) + tile_off<D>(arow, 2 * k + ach), qk);
+                if constexpr (!QREG) ldsm4(sq0 + swizzled_off(RT, arow, 2 * k + ach), qk);
 #pragma unroll
                 for (int c = 0; c < NC; c++) {
                     uint32_t b[4];
                     const int row = wn * (NC * 16) + c * 16 + (lane & 7) + ((lane >> 4) << 3);
-                    ldsm4(sk + tile_off<D>(row, 2 * k + ((lane >> 3) & 1)), b);
-                    if constexpr (QREG) {
-                        mma16816(s[c][0], qf[k], b[0], b[1]);
-                        mma16816(s[c][1], qf[k], b[2], b[3]);
-                    } else {
-                        mma16816(s[c][0], qk, b[0], b[1]);
-                        mma16816(s[c][1], qk, b[2], b[3]);
-                    }
+                    ldsm4(sk + swizzled_off(T, row, 2 * k + ((lane >> 3) & 1)), b);
+                    mma16816(s[c][0][k & 1], QREG ? qf[QREG ? k : 0] : qk, b[0], b[1]);
+                    mma16816(s[c][1][k & 1], QREG ? qf[QREG ? k : 0] : qk, b[2], b[3]);
                 }
             }
             // ---- running softmax in powers of two
+            const bool edge = tok0 < all_lo || tok0 + NC * 16 > all_hi;
             float mx[2] = { m[0], m[1] };
 #pragma unroll
             for (int c = 0; c < NC; c++)
@@ -309,10 +345,14 @@ __global__ void __launch_bounds__(kFewThreads) paged_few_kernel(const PagedArgs 
                 for (int n = 0; n < 2; n++)
 #pragma unroll
                     for (int k = 0; k < 4; k++) {
-                        const int tok = tok0 + c * 16 + n * 8 + (lane & 3) * 2 + (k & 1), i = k >> 1;
-                        const float x = s[c][n][k] * a.scale_log2;
-                        s[c][n][k] = tok >= rlo[i] && tok < rhi[i] ? x : -INFINITY;
-                        mx[i] = fmaxf(mx[i], s[c][n][k]);
+                        const int i = k >> 1;
+                        float x = (s[c][n][0][k] + s[c][n][1][k]) * a.scale_log2;
+                        if (edge) {
+                            const int tok = tok0 + c * 16 + n * 8 + (lane & 3) * 2 + (k & 1);
+                            x = tok >= rlo[i] && tok < rhi[i] ? x : -INFINITY;
+                        }
+                        s[c][n][0][k] = x;
+                        mx[i] = fmaxf(mx[i], x);
                     }
             float base[2];
             bool grow = false;
@@ -336,6 +376,21 @@ __global__ void __launch_bounds__(kFewThreads) paged_few_kernel(const PagedArgs 
                     }
                 }
             }
+            if (edge) {
+                // rows of V outside the job's tokens meet weight 0, whatever
+                // the slots (or the ring, where nothing was copied) hold
+                const int from = max(w.lo - tok0, 0), to = w.hi - tok0;
+                if (from > 0 || to < NC * 16) {
+                    for (int e = lane; e < NC * 16 * (D / 8); e += 32) {
+                        const int r = e / (D / 8), c = e % (D / 8);
+                        if (r < from || r >= to)
+                            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(sv + swizzled_off(T, wn * (NC * 16) + r, c)),
+                                         "r"(0u) : "memory");
+                    }
+                    fence_async_smem();  // before the next copy into this stage
+                    __syncwarp();
+                }
+            }
 #pragma unroll
             for (int c = 0; c < NC; c++) {
                 // weights are rounded to bf16 for the product with V (2^-8 of
@@ -344,23 +399,26 @@ __global__ void __launch_bounds__(kFewThreads) paged_few_kernel(const PagedArgs 
                 for (int n = 0; n < 2; n++)
 #pragma unroll
                     for (int k = 0; k < 4; k++) {
-                        s[c][n][k] = ex2(s[c][n][k] - base[k >> 1]);
-                        l[k >> 1] += s[c][n][k];
+                        s[c][n][0][k] = ex2(s[c][n][0][k] - base[k >> 1]);
+                        l[k >> 1] += s[c][n][0][k];
                     }
-                const uint32_t p[4] = { pack2(s[c][0][0], s[c][0][1]), pack2(s[c][0][2], s[c][0][3]),
-                                        pack2(s[c][1][0], s[c][1][1]), pack2(s[c][1][2], s[c][1][3]) };
+                const uint32_t p[4] = { pack2(s[c][0][0][0], s[c][0][0][1]), pack2(s[c][0][0][2], s[c][0][0][3]),
+                                        pack2(s[c][1][0][0], s[c][1][0][1]), pack2(s[c][1][0][2], s[c][1][0][3]) };
                 const int row = wn * (NC * 16) + c * 16 + (lane & 15);
 #pragma unroll
                 for (int n = 0; n < D / 16; n++) {
                     uint32_t b[4];
-                    ldsm4t(sv + tile_off<D>(row, 2 * n + (lane >> 4)), b);
+                    ldsm4t(sv + swizzled_off(T, row, 2 * n + (lane >> 4)), b);
                     mma16816(o[2 * n], p, b[0], b[1]);
                     mma16816(o[2 * n + 1], p, b[2], b[3]);
                 }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty(stage));
+            advance();
         }
-        cp_wait<0>();
-        __syncthreads();  // the ring is free: it takes the warps' outputs
+        if (!ok && lane == 0 && a.status) atomicOr(a.status, kStatusTimeout);
+        __syncthreads();  // (A) every tile is read: the ring takes the warps' outputs
 
         // ---- join the warps of the same rows
         float *so = reinterpret_cast<float *>(ring);  // [WN][RT][D]
@@ -378,11 +436,11 @@ __global__ void __launch_bounds__(kFewThreads) paged_few_kernel(const PagedArgs 
                 *reinterpret_cast<float2 *>(so + ((wn * RT + 16 * wm + r) * D + ((8 * n) ^ ((r & 7) << 3)) + (lane & 3) * 2)) =
                     make_float2(o[n][2 * i], o[n][2 * i + 1]);
         }
-        __syncthreads();
-        const bool whole = w.whole();
-        float *mine = a.part + (int64_t)w.slot() * (RT * (D + 2));
+        consumers_sync();
+        const bool whole = CLUSTER || w.whole();
+        float *mine = CLUSTER ? nullptr : a.part + (int64_t)w.slot() * (RT * (D + 2));
         constexpr int C4 = D / 4;
-        for (int e = tid; e < nr * C4; e += kFewThreads) {
+        for (int e = tid; e < nr * C4; e += kFewRows) {
             const int r = e / C4, c = e % C4;
             float mt = -INFINITY, lt = 0.0f;
 #pragma unroll
@@ -400,7 +458,13 @@ __global__ void __launch_bounds__(kFewThreads) paged_few_kernel(const PagedArgs 
                 acc.z += f * v.z;
                 acc.w += f * v.w;
             }
-            if (whole) {
+            if (CLUSTER) {  // in place, over the first warp's share
+                *reinterpret_cast<float4 *>(so + r * D + ((4 * c) ^ ((r & 7) << 3))) = acc;
+                if (c == 0) {
+                    s_fm[r] = mt;
+                    s_fl[r] = lt;
+                }
+            } else if (whole) {
                 finish_row(a, w.s.q0, w.h, r0 + r, c, acc, mt, lt);
             } else {
                 *reinterpret_cast<float4 *>(mine + 2 * RT + r * D + 4 * c) = acc;
@@ -410,22 +474,56 @@ __global__ void __launch_bounds__(kFewThreads) paged_few_kernel(const PagedArgs 
                 }
             }
         }
-        if (!whole) {
+        if constexpr (CLUSTER) {
+            const int rank = (int)blockIdx.x % a.split;
+            cluster_sync();
+            for (int e = rank * kFewRows + tid; e < nr * C4; e += a.split * kFewRows) {
+                const int r = e / C4, c = e % C4;
+                const uint32_t am = smem_u32(s_fm + r), al = smem_u32(s_fl + r),
+                               ao = smem_u32(so + r * D + ((4 * c) ^ ((r & 7) << 3)));
+                float mt = -INFINITY;
+#pragma unroll 8
+                for (int k = 0; k < a.split; k++) mt = fmaxf(mt, cluster_ld(cluster_map(am, k)));
+                const float bs = mt == -INFINITY ? 0.0f : mt;
+                float lt = 0.0f;
+                float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+                for (int k = 0; k < a.split; k++) {
+                    const float f = ex2(cluster_ld(cluster_map(am, k)) - bs);
+                    lt = fmaf(f, cluster_ld(cluster_map(al, k)), lt);
+                    const float4 v = cluster_ld4(cluster_map(ao, k));
+                    acc.x = fmaf(f, v.x, acc.x);
+                    acc.y = fmaf(f, v.y, acc.y);
+                    acc.z = fmaf(f, v.z, acc.z);
+                    acc.w = fmaf(f, v.w, acc.w);
+                }
+                finish_row(a, w.s.q0, w.h, r0 + r, c, acc, mt, lt);
+            }
+        } else if (!whole) {
             __threadfence();
-            __syncthreads();
+            consumers_sync();
             const int c0 = w.owner(), c1 = w.last();
             if (tid == 0) s_last = atomicAdd(a.counter + c0, 1u) == (unsigned)(c1 - c0);
-            __syncthreads();
+            consumers_sync();
             if (s_last) {
                 __threadfence();
-                for (int e = tid; e < nr * C4; e += kFewThreads) {
+                for (int e = tid; e < nr * C4; e += kFewRows) {
                     const int r = e / C4, c = e % C4;
                     join_parts<RT, D>(a, w.s.q0, w.h, r0 + r, r, c, c0, c1);
                 }
             }
         }
-        __syncthreads();  // shared memory is free for the next segment
-    } while (w.next(a));
+        if constexpr (!CLUSTER) {
+            fence_async_smem();
+            ok = !__syncthreads_or(!ok);  // (B) the ring is free for the next segment's copies
+        }
+        }
+        if constexpr (CLUSTER) {
+            if (warp == kFewWarps) cluster_sync();
+            cluster_sync();  // no block leaves while another reads its shared memory
+            return;
+        }
+    } while (ok && w.next(a));
 }
 
 // ------------------------------------------------------------ join
@@ -500,10 +598,23 @@ namespace {
 template <int D, int WM>
 cudaError_t launch_few(const PagedArgs &a, cudaStream_t s)
 {
+    CUtensorMap kmap, vmap;
+    const int box = (1 << a.page_shift) < kFewT ? 1 << a.page_shift : kFewT;
+    cudaError_t t = page_map(&kmap, a, a.k, D, box);
+    if (t == cudaSuccess) t = page_map(&vmap, a, a.v, D, box);
+    if (t != cudaSuccess) return t;
     constexpr int smem = (int)few_smem<D, WM>();
-    const cudaError_t e = cudaFuncSetAttribute(paged_few_kernel<D, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (a.split) {
+        const auto kern = paged_few_kernel<D, WM, true>;
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess && a.split > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        return launch_clusters(kern, a.grid, a.split, kFewThreads, smem, s, a, kmap, vmap);
+    }
+    const auto kern = paged_few_kernel<D, WM, false>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(paged_few_kernel<D, WM>, a.grid, kFewThreads, smem, s, a);
+    return launch_dependent(kern, a.grid, kFewThreads, smem, s, a, kmap, vmap);
 }
 
 template <int D>
@@ -565,7 +676,22 @@ PagedPlan paged_plan(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_k
         p.few.rows = many || rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
         p.few.row_hi = many ? 16 : INT32_MAX;
         p.few.grid = sm_count() * (head_dim == 64 ? 3 : head_dim == 128 ? 2 : 1);
-        place(p.few, 1);
+        // One launch in clusters where the blocks of all jobs fit at once and
+        // uneven lengths cannot make one cluster late: a single sequence (its
+        // jobs are alike), or few tiles per block.
+        const int64_t row_tiles = (rows + p.few.rows - 1) / p.few.rows, tiles = (max_kv + kFewT - 1) / kFewT;
+        const int64_t jobs = batch * heads * row_tiles;
+        if (!many && jobs > 0 && jobs <= p.few.grid) {
+            int split = 1;
+            while (split < 16 && 2 * split * jobs <= p.few.grid && split < tiles) split *= 2;
+            const int64_t per_block = (tiles + split - 1) / split;
+            if (per_block <= kClusterTiles || (batch == 1 && 2 * split * jobs >= sm_count())) {
+                p.few.split = split;
+                p.few.row_tiles = (int)row_tiles;
+                p.few.grid = (int)(jobs * split);
+            }
+        }
+        if (!p.few.split) place(p.few, 1);
     }
     if (many) {
         p.many.rows = paged_many_rows(head_dim);
@@ -574,7 +700,7 @@ PagedPlan paged_plan(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_k
         p.many.grid = sm_count();
         place(p.many, p.many.rows / 128);
     }
-    p.total = at;
+    p.total = at > 256 ? at : 256;
     return p;
 }
 
@@ -590,6 +716,8 @@ cudaError_t launch_paged(const PagedArgs &args, const PagedPlan &p, int head_dim
         a.grid = k.grid;
         a.row_lo = k.row_lo;
         a.row_hi = k.row_hi;
+        a.split = k.split;
+        a.row_tiles = k.row_tiles;
         return a;
     };
     PagedArgs a = share(p.few);
@@ -602,7 +730,7 @@ cudaError_t launch_paged(const PagedArgs &args, const PagedPlan &p, int head_dim
         if (e == cudaSuccess) e = launch_paged_many(b, head_dim, s);
         if (!p.few.grid) return e;
     } else {
-        e = launch_plan_few(a, p.few.rows, s);
+        e = a.split ? cudaSuccess : launch_plan_few(a, p.few.rows, s);
     }
     if (e != cudaSuccess) return e;
     switch (head_dim) {

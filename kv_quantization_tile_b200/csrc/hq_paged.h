@@ -85,6 +85,7 @@ struct PagedArgs {
     uint32_t *counter;       // [grid] finished parts of the job whose first tile block c holds
     float *part;             // [2 grid] partial results
     int grid, min_tiles;     // blocks; least tiles a block takes
+    int split, row_tiles;    // clusters (no plan): blocks of a job, row tiles of the longest sequence
     int32_t *status;
 };
 
@@ -92,6 +93,7 @@ struct PagedArgs {
 struct PagedShare {
     int grid, rows;                // blocks (0: not launched), rows per row tile
     int row_lo, row_hi;            // the sequences it takes (rows: new tokens x group)
+    int split, row_tiles;          // clusters of `split` blocks, one job each (0: planned shares)
     uint64_t prefix, start, counter, part;  // offsets
 };
 
@@ -210,6 +212,25 @@ struct SegWalk {
         return true;
     }
 
+    // Without a plan: a cluster of `split` blocks takes one job, each an equal
+    // share of its tokens (possibly none).
+    __device__ __forceinline__ bool begin_cluster(const PagedArgs &a)
+    {
+        const int job = (int)blockIdx.x / a.split, rank = (int)blockIdx.x - job * a.split;
+        const int bh = job / a.row_tiles;
+        rt = job - bh * a.row_tiles;
+        b = bh / a.heads;
+        h = bh - b * a.heads;
+        bool bad;
+        s = load_seq(a, b, bad);
+        if (bad && rank == 0 && h == 0 && rt == 0 && threadIdx.x == 0 && a.status) atomicOr(a.status, kStatusIndex);
+        if (rt * RT >= s.rows) return false;
+        job_tiles<T, RT>(a, s, rt, t0, n, lo, hi);
+        first = (int)((int64_t)n * rank / a.split);
+        count = (int)((int64_t)n * (rank + 1) / a.split) - first;
+        return true;
+    }
+
     __device__ __forceinline__ bool whole() const { return count == n; }
     __device__ __forceinline__ int block_of(int64_t g) const { return (int)(((g + 1) * grid - 1) / total); }
     // blocks that hold a part of this job
@@ -282,6 +303,32 @@ __device__ __forceinline__ void join_parts(const PagedArgs &a, int q0, int h, in
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// ------------------------------------------------------------ clusters
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// the address in block `rank`'s shared memory that corresponds to `addr` here
+__device__ __forceinline__ uint32_t cluster_map(uint32_t addr, int rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float cluster_ld(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 cluster_ld4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
 // Launch a kernel that may become resident before the one in front of it ends
 // (it waits for that one's results with pdl_wait).
 template <typename... P>
@@ -295,6 +342,24 @@ inline cudaError_t launch_dependent(void (*kern)(P...), int grid, int threads, s
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// Launch a kernel in clusters of `size` blocks.
+template <typename... P>
+inline cudaError_t launch_clusters(void (*kern)(P...), int grid, int size, int threads, size_t smem, cudaStream_t s, P... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)size;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, args...);

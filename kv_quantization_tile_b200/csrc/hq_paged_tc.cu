@@ -27,11 +27,8 @@
 // takes 2048 clocks of tensor pipe and 2048 of exponentials.
 #include <atomic>
 
-#include <cuda.h>
-
 #include "hq_fast.cuh"
-#include "hq_paged.h"
-#include "hq_tcgen05.cuh"
+#include "hq_paged_tma.cuh"
 
 namespace hq {
 
@@ -124,28 +121,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ void mbar_arrive(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes)
-{
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap *map, uint32_t bar, int col, int slot, int head, int page)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
-        ::"r"(dst), "l"(map), "r"(bar), "r"(col), "r"(slot), "r"(head), "r"(page)
-        : "memory");
-}
-
-__device__ __forceinline__ uint32_t pack2(float lo, float hi)
-{
-    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&p);
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float d;
@@ -206,13 +181,6 @@ __device__ __forceinline__ bool named_any(int id, int threads, bool v)
         : "r"(id), "r"(threads), "r"((uint32_t)v)
         : "memory");
     return any;
-}
-
-// byte offset of 16-byte chunk c of row r in a 128-byte-swizzled operand of
-// `rows` rows: blocks of 64 columns, each [rows][128 bytes]
-__device__ __forceinline__ uint32_t swizzled_off(int rows, int r, int c)
-{
-    return (uint32_t)((c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
 }  // namespace
@@ -740,8 +708,8 @@ EncodeTiled encode_tiled()
     return f;
 }
 
-// A pool as [page][head][slot][d]: one copy takes up to `box` slots of 64
-// columns; a page past the pool reads zeros.
+}  // namespace
+
 cudaError_t page_map(CUtensorMap *m, const PagedArgs &a, const void *pool, int d, int box)
 {
     const EncodeTiled encode = encode_tiled();
@@ -755,6 +723,8 @@ cudaError_t page_map(CUtensorMap *m, const PagedArgs &a, const void *pool, int d
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? cudaSuccess : cudaErrorInvalidValue;
 }
+
+namespace {
 
 template <int D>
 cudaError_t launch_many_d(const PagedArgs &a, cudaStream_t s)
