@@ -18,9 +18,10 @@ namespace hq {
 
 namespace {
 
-constexpr int kFewWarps = 4, kFewRows = 32 * kFewWarps;    // consumer warps and their threads
-constexpr int kFewThreads = kFewRows + 32, kFewT = 64;      // and one warp that loads
+constexpr int kFewT = 64;          // tokens per tile of the planned kernel
 constexpr int kPlanThreads = 1024;
+// A job's own cost in tiles (prologue and results), for equal shares
+constexpr int kJobCostFew = 2, kJobCostMany = 2;
 constexpr int kClusterTiles = 16;  // most tiles a block takes of an uneven batch without a plan
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4])
@@ -41,56 +42,63 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kFewRows) : "memory"); }
+template <int THREADS>
+__device__ __forceinline__ void named_sync1() { asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory"); }
 
-// stages of K and V tiles: about 64 KB in flight per SM keep HBM busy
-template <int D>
-constexpr int few_stages() { return D == 64 ? 4 : 3; }
-// blocks per SM that shared memory and registers allow
-template <int D>
-constexpr int few_blocks() { return D == 64 ? 3 : D == 128 ? 2 : 1; }
-template <int D, int WM>
-constexpr size_t few_smem() { return 1024 + (D == 256 ? 16 * WM * D * 2 : 0) + (size_t)few_stages<D>() * 2 * kFewT * D * 2; }
+// W consumer warps and one that loads; tiles of 16 W tokens; a row tile of 16 WM rows
+template <int D, int WM, int W>
+struct Few {
+    static constexpr int T = 16 * W, RT = 16 * WM, ROWS = 32 * W, THREADS = ROWS + 32;
+    // stages of K and V tiles: about 64 KB in flight per SM keep HBM busy
+    static constexpr int STAGES = D == 64 ? 4 : 3;
+    // blocks per SM that shared memory and registers allow
+    static constexpr int BLOCKS = W > 4 ? 1 : D == 64 ? 3 : D == 128 ? 2 : 1;
+    static constexpr uint32_t TILE = T * D * 2;
+    static constexpr size_t SMEM = 1024 + (D == 256 ? RT * D * 2 : 0) + (size_t)STAGES * 2 * TILE;
+};
 
 }  // namespace
 
 // ------------------------------------------------------------ plan
-// Tiles before each sequence, the place where each block's share begins, and
-// cleared counters.  One block; a warp counts a sequence's row tiles.
+// Units of work (tiles, and each job's own cost) before each sequence, the place where each block's share begins, and
+// cleared counters.  One block, a chunk of 1024 sequences at a time: a thread
+// counts a sequence's units (a warp, where sequences have many row tiles).
 template <int T, int RT>
 __device__ __forceinline__ void plan_share(const PagedArgs &a, const int parts)
 {
-    __shared__ int64_t w[kPlanThreads];
+    __shared__ int64_t pre[kPlanThreads];      // units of each sequence of the chunk, then before it
     __shared__ int64_t wsum[kPlanThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int c = tid; c < a.grid * parts; c += kPlanThreads) a.counter[c] = 0u;
+    const bool by_warp = a.max_q * (int64_t)a.group > 8 * RT;
     int64_t before = 0;
     for (int b0 = 0; b0 < a.batch; b0 += kPlanThreads) {
-        for (int i = warp; i < kPlanThreads; i += kPlanThreads / 32) {
-            const int b = b0 + i;
+        const int nb = min(kPlanThreads, a.batch - b0);
+        auto count = [&](int i, int rt0, int step) -> int64_t {
+            bool bad;
+            const Seq s = load_seq(a, b0 + i, bad);
+            if (bad && rt0 == 0 && a.status) atomicOr(a.status, kStatusIndex);
             int64_t tiles = 0;
-            if (b < a.batch) {
-                bool bad;
-                const Seq s = load_seq(a, b, bad);
-                if (bad && lane == 0 && a.status) atomicOr(a.status, kStatusIndex);
-                const int nrt = (s.rows + RT - 1) / RT;
-                for (int rt = lane; rt < nrt; rt += 32) {
-                    int t0, n, lo, hi;
-                    job_tiles<T, RT>(a, s, rt, t0, n, lo, hi);
-                    tiles += n;
-                }
+            for (int rt = rt0; rt * RT < s.rows; rt += step) {
+                int t0, n, lo, hi;
+                job_tiles<T, RT>(a, s, rt, t0, n, lo, hi);
+                tiles += n + a.job_cost;
             }
+            return tiles * a.heads;
+        };
+        int64_t mine = 0;
+        if (by_warp) {
+            for (int i = warp; i < nb; i += kPlanThreads / 32) {
+                int64_t tiles = count(i, lane, 32);
 #pragma unroll
-            for (int m = 16; m >= 1; m >>= 1) tiles += __shfl_xor_sync(FULL, tiles, m);
-            if (lane == 0) w[i] = tiles * a.heads;
-            if (b0 + i + kPlanThreads / 32 >= a.batch) {  // the rest of the chunk is past the last sequence
-                for (int k = i + kPlanThreads / 32; k < kPlanThreads; k += kPlanThreads / 32)
-                    if (lane == 0) w[k] = 0;
-                break;
+                for (int m = 16; m >= 1; m >>= 1) tiles += __shfl_xor_sync(FULL, tiles, m);
+                if (lane == 0) pre[i] = tiles;
             }
+            __syncthreads();
+            if (tid < nb) mine = pre[tid];
+        } else if (tid < nb) {
+            mine = count(tid, 0, 1);
         }
-        __syncthreads();
-        const int64_t mine = w[tid];
         int64_t incl = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -99,30 +107,37 @@ __device__ __forceinline__ void plan_share(const PagedArgs &a, const int parts)
         }
         if (lane == 31) wsum[warp] = incl;
         __syncthreads();
-        int64_t base = before, all = before;
-        for (int k = 0; k < kPlanThreads / 32; k++) {
-            if (k < warp) base += wsum[k];
-            all += wsum[k];
+        int64_t sums = wsum[lane];  // every warp scans the warps' sums
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t o = __shfl_up_sync(FULL, sums, d);
+            if (lane >= d) sums += o;
         }
-        if (b0 + tid < a.batch) a.prefix[b0 + tid] = base + incl - mine;
-        before = all;
+        const int64_t base = before + (warp ? __shfl_sync(FULL, sums, warp - 1) : 0);
+        pre[tid] = base + incl - mine;
+        if (tid < nb) a.prefix[b0 + tid] = pre[tid];
+        before += __shfl_sync(FULL, sums, 31);
         __syncthreads();
     }
-    if (tid == 0) a.prefix[a.batch] = before;
-    __syncthreads();
     const int64_t total = before;
+    if (tid == 0) a.prefix[a.batch] = total;
     if (total == 0) return;
-    const int grid = (int)min((int64_t)a.grid, (total + a.min_tiles - 1) / a.min_tiles);
+    if (a.batch > kPlanThreads) __syncthreads();  // prefix is read back
+    const int grid = (int)min((int64_t)a.grid, (total + a.min_units - 1) / a.min_units);
+    auto prefix = [&](int b) -> int64_t {
+        if (b == a.batch) return total;
+        return a.batch <= kPlanThreads ? pre[b] : a.prefix[b];
+    };
     for (int c = tid; c < grid; c += kPlanThreads) {
         const int64_t at = total * c / grid;
-        int lo = 0, hi = a.batch - 1;  // the last sequence that begins at or before `at` and has tiles
+        int lo = 0, hi = a.batch - 1;  // the last sequence that begins at or before `at` and has units
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (a.prefix[mid] <= at) lo = mid;
+            if (prefix(mid) <= at) lo = mid;
             else hi = mid - 1;
         }
-        const int64_t per_head = (a.prefix[lo + 1] - a.prefix[lo]) / a.heads;
-        int64_t rest = at - a.prefix[lo];
+        const int64_t per_head = (prefix(lo + 1) - prefix(lo)) / a.heads;
+        int64_t rest = at - prefix(lo);
         PagedStart st;
         st.b = lo;
         st.h = (int)(rest / per_head);
@@ -132,10 +147,11 @@ __device__ __forceinline__ void plan_share(const PagedArgs &a, const int parts)
         for (st.rt = 0;; st.rt++) {
             int t0, n, l, h;
             job_tiles<T, RT>(a, s, st.rt, t0, n, l, h);
-            if (rest < n || (st.rt + 1) * RT >= s.rows) break;
-            rest -= n;
+            if (rest < n + a.job_cost || (st.rt + 1) * RT >= s.rows) break;
+            rest -= n + a.job_cost;
         }
-        st.tile = (int)rest;
+        st.job = at - rest;
+        st.tile = rest > a.job_cost ? (int)rest - a.job_cost : 0;
         a.start[c] = st;
     }
 }
@@ -151,27 +167,28 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedArg
 }
 
 // ------------------------------------------------------------ few rows
-// Four consumer warps; a row tile has 16 WM rows.  Warp (wm, wn) multiplies rows
+// W consumer warps; a row tile has 16 WM rows.  Warp (wm, wn) multiplies rows
 // 16 wm .. with its share of each tile's tokens and keeps its own running
-// softmax; the 4 / WM warps of the same rows are joined after the last tile.  A
-// fifth warp copies the tiles' pages with TMA into a ring of stages, so the
+// softmax; the W / WM warps of the same rows are joined after the last tile.  One
+// more warp copies the tiles' pages with TMA into a ring of stages, so the
 // consumers meet no one else between tiles: each waits for a stage's bytes and
 // reports when it has read them.  (With the tiles copied by the consumers
 // themselves, 16 bytes a thread, and a block barrier per tile, a tile took 2500
 // clocks, most of them addresses and waiting.)
 // CLUSTER: no plan; the blocks of a cluster share one job, and join their
 // results through each other's shared memory.
-template <int D, int WM, bool CLUSTER>
-__global__ void __launch_bounds__(kFewThreads, few_blocks<D>())
+template <int D, int WM, int W, bool CLUSTER>
+__global__ void __launch_bounds__(Few<D, WM, W>::THREADS, Few<D, WM, W>::BLOCKS)
 paged_few_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
 {
-    constexpr int T = kFewT, RT = 16 * WM, WN = 4 / WM, NC = T / WN / 16;  // NC: 16-token chunks per warp and tile
-    constexpr int STAGES = few_stages<D>(), KS = D / 16;
-    constexpr uint32_t TILE = T * D * 2;
+    using F = Few<D, WM, W>;
+    constexpr int T = F::T, RT = F::RT, ROWS = F::ROWS, STAGES = F::STAGES, KS = D / 16;
+    constexpr int WN = W / WM, NC = T / WN / 16;  // NC: 16-token chunks per warp and tile
+    constexpr uint32_t TILE = F::TILE;
     constexpr bool QREG = D <= 128;  // q fragments stay in registers
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t s_bar[2 * STAGES];
-    __shared__ float s_m[4][16], s_l[4][16];
+    __shared__ float s_m[W][16], s_l[W][16];
     __shared__ float s_fm[CLUSTER ? RT : 1], s_fl[CLUSTER ? RT : 1];
     __shared__ int s_last;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -183,7 +200,7 @@ paged_few_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, co
     if (tid == 0) {
         for (int s = 0; s < STAGES; s++) {
             mbar_init(full(s), 1);
-            mbar_init(empty(s), kFewWarps);
+            mbar_init(empty(s), W);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -208,7 +225,7 @@ paged_few_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, co
     do {
         const int r0 = w.rt * RT, nr = min(RT, w.s.rows - r0);
         const int end = w.first + w.count;
-        if (warp == kFewWarps) {
+        if (warp == W) {
             // -------------------------------------------- loads
             const int page_rows = 1 << a.page_shift, box = page_rows < T ? page_rows : T;
             const int col = lane % (D / 64), pg = lane / (D / 64);
@@ -268,7 +285,7 @@ paged_few_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, co
                 for (int i = 0; i < 4; i++)
                     qf[k][i] = q[i & 1] ? *reinterpret_cast<const uint32_t *>(q[i & 1] + 16 * k + 8 * (i >> 1) + 2 * (lane & 3)) ^ flip : 0u;
         } else {
-            for (int e = tid; e < RT * (D / 8); e += kFewRows) {
+            for (int e = tid; e < RT * (D / 8); e += ROWS) {
                 const int r = e / (D / 8), c = e % (D / 8);
                 const uint16_t *q = query(r);
                 uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -278,7 +295,7 @@ paged_few_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, co
                 }
                 *reinterpret_cast<uint4 *>(sq + swizzled_off(RT, r, c)) = v;
             }
-            consumers_sync();
+            named_sync1<ROWS>();
         }
         // the tokens each of this thread's two rows sees, and those all of the
         // warp's rows see
@@ -436,11 +453,11 @@ paged_few_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, co
                 *reinterpret_cast<float2 *>(so + ((wn * RT + 16 * wm + r) * D + ((8 * n) ^ ((r & 7) << 3)) + (lane & 3) * 2)) =
                     make_float2(o[n][2 * i], o[n][2 * i + 1]);
         }
-        consumers_sync();
+        named_sync1<ROWS>();
         const bool whole = CLUSTER || w.whole();
         float *mine = CLUSTER ? nullptr : a.part + (int64_t)w.slot() * (RT * (D + 2));
         constexpr int C4 = D / 4;
-        for (int e = tid; e < nr * C4; e += kFewRows) {
+        for (int e = tid; e < nr * C4; e += ROWS) {
             const int r = e / C4, c = e % C4;
             float mt = -INFINITY, lt = 0.0f;
 #pragma unroll
@@ -477,7 +494,7 @@ paged_few_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, co
         if constexpr (CLUSTER) {
             const int rank = (int)blockIdx.x % a.split;
             cluster_sync();
-            for (int e = rank * kFewRows + tid; e < nr * C4; e += a.split * kFewRows) {
+            for (int e = rank * ROWS + tid; e < nr * C4; e += a.split * ROWS) {
                 const int r = e / C4, c = e % C4;
                 const uint32_t am = smem_u32(s_fm + r), al = smem_u32(s_fl + r),
                                ao = smem_u32(so + r * D + ((4 * c) ^ ((r & 7) << 3)));
@@ -501,16 +518,13 @@ paged_few_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, co
             }
         } else if (!whole) {
             __threadfence();
-            consumers_sync();
-            const int c0 = w.owner(), c1 = w.last();
+            named_sync1<ROWS>();
+            const int c0 = w.owner(a), c1 = w.last(a);
             if (tid == 0) s_last = atomicAdd(a.counter + c0, 1u) == (unsigned)(c1 - c0);
-            consumers_sync();
+            named_sync1<ROWS>();
             if (s_last) {
                 __threadfence();
-                for (int e = tid; e < nr * C4; e += kFewRows) {
-                    const int r = e / C4, c = e % C4;
-                    join_parts<RT, D>(a, w.s.q0, w.h, r0 + r, r, c, c0, c1);
-                }
+                join_parts<RT, D, ROWS>(a, w.s.q0, w.h, r0, nr, tid, c0, c1);
             }
         }
         if constexpr (!CLUSTER) {
@@ -519,7 +533,7 @@ paged_few_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, co
         }
         }
         if constexpr (CLUSTER) {
-            if (warp == kFewWarps) cluster_sync();
+            if (warp == W) cluster_sync();
             cluster_sync();  // no block leaves while another reads its shared memory
             return;
         }
@@ -595,35 +609,39 @@ __global__ void __launch_bounds__(256) merge_kernel(const MergeArgs a)
 // ------------------------------------------------------------ launch
 namespace {
 
-template <int D, int WM>
+template <int D, int WM, int W, bool CLUSTER>
 cudaError_t launch_few(const PagedArgs &a, cudaStream_t s)
 {
+    using F = Few<D, WM, W>;
     CUtensorMap kmap, vmap;
-    const int box = (1 << a.page_shift) < kFewT ? 1 << a.page_shift : kFewT;
-    cudaError_t t = page_map(&kmap, a, a.k, D, box);
-    if (t == cudaSuccess) t = page_map(&vmap, a, a.v, D, box);
-    if (t != cudaSuccess) return t;
-    constexpr int smem = (int)few_smem<D, WM>();
-    if (a.split) {
-        const auto kern = paged_few_kernel<D, WM, true>;
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e == cudaSuccess && a.split > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-        return launch_clusters(kern, a.grid, a.split, kFewThreads, smem, s, a, kmap, vmap);
-    }
-    const auto kern = paged_few_kernel<D, WM, false>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const int box = (1 << a.page_shift) < F::T ? 1 << a.page_shift : F::T;
+    const auto kern = paged_few_kernel<D, WM, W, CLUSTER>;
+    cudaError_t e = page_map(&kmap, a, a.k, D, box);
+    if (e == cudaSuccess) e = page_map(&vmap, a, a.v, D, box);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)F::SMEM);
+    if (e == cudaSuccess && CLUSTER && a.split > 8)
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kern, a.grid, kFewThreads, smem, s, a, kmap, vmap);
+    if (CLUSTER) return launch_clusters(kern, a.grid, a.split, F::THREADS, F::SMEM, s, a, kmap, vmap);
+    return launch_dependent(kern, a.grid, F::THREADS, F::SMEM, s, a, kmap, vmap);
+}
+
+template <int D, int WM>
+cudaError_t launch_few_m(const PagedArgs &a, int warps, cudaStream_t s)
+{
+    if (!a.split) return launch_few<D, WM, 4, false>(a, s);
+    if constexpr (WM == 1 && D <= 128)
+        if (warps == 8) return launch_few<D, WM, 8, true>(a, s);
+    return launch_few<D, WM, 4, true>(a, s);
 }
 
 template <int D>
-cudaError_t launch_few_d(const PagedArgs &a, int rows, cudaStream_t s)
+cudaError_t launch_few_d(const PagedArgs &a, int rows, int warps, cudaStream_t s)
 {
     switch (rows) {
-    case 16: return launch_few<D, 1>(a, s);
-    case 32: return launch_few<D, 2>(a, s);
-    default: return launch_few<D, 4>(a, s);
+    case 16: return launch_few_m<D, 1>(a, warps, s);
+    case 32: return launch_few_m<D, 2>(a, warps, s);
+    default: return launch_few_m<D, 4>(a, warps, s);
     }
 }
 
@@ -655,7 +673,8 @@ cudaError_t launch_plan_many(const PagedArgs &many, const PagedArgs &few, int he
 // beside a prompt) still go to the other one.  Blocks: as many as are resident
 // at once (shared memory allows 3, 2 and 1 of the mma.sync kernel per SM at
 // head_dim 64, 128 and 256, one of the tcgen05 kernel).
-PagedPlan paged_plan(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_kv, int heads, int group, int head_dim)
+PagedPlan paged_plan(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_kv, int heads, int group, int head_dim,
+                     int64_t window)
 {
     PagedPlan p{};
     const int64_t rows = max_q * group;
@@ -679,7 +698,11 @@ PagedPlan paged_plan(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_k
         // One launch in clusters where the blocks of all jobs fit at once and
         // uneven lengths cannot make one cluster late: a single sequence (its
         // jobs are alike), or few tiles per block.
-        const int64_t row_tiles = (rows + p.few.rows - 1) / p.few.rows, tiles = (max_kv + kFewT - 1) / kFewT;
+        // At one block per SM the block has eight consumer warps (16 rows, head_dim
+        // up to 128): four leave a tile's chain of dependent steps exposed.
+        const int64_t row_tiles = (rows + p.few.rows - 1) / p.few.rows;
+        const int64_t reach = window > 0 && window + max_q < max_kv ? window + max_q : max_kv;  // tokens a job reads
+        const int64_t tiles = (reach + kFewT - 1) / kFewT + (reach < max_kv ? 1 : 0);
         const int64_t jobs = batch * heads * row_tiles;
         if (!many && jobs > 0 && jobs <= p.few.grid) {
             int split = 1;
@@ -689,6 +712,7 @@ PagedPlan paged_plan(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_k
                 p.few.split = split;
                 p.few.row_tiles = (int)row_tiles;
                 p.few.grid = (int)(jobs * split);
+                p.few.warps = p.few.rows == 16 && head_dim <= 128 && p.few.grid <= sm_count() && per_block >= 4 ? 8 : 4;
             }
         }
         if (!p.few.split) place(p.few, 1);
@@ -721,11 +745,13 @@ cudaError_t launch_paged(const PagedArgs &args, const PagedPlan &p, int head_dim
         return a;
     };
     PagedArgs a = share(p.few);
-    a.min_tiles = 2;
+    a.job_cost = kJobCostFew;
+    a.min_units = kJobCostFew + 2;
     cudaError_t e;
     if (p.many.grid) {
         PagedArgs b = share(p.many);
-        b.min_tiles = 4;
+        b.job_cost = kJobCostMany;
+        b.min_units = kJobCostMany + 4;
         e = launch_plan_many(b, a, head_dim, p.few.grid > 0, s);
         if (e == cudaSuccess) e = launch_paged_many(b, head_dim, s);
         if (!p.few.grid) return e;
@@ -734,9 +760,9 @@ cudaError_t launch_paged(const PagedArgs &args, const PagedPlan &p, int head_dim
     }
     if (e != cudaSuccess) return e;
     switch (head_dim) {
-    case 64: return launch_few_d<64>(a, p.few.rows, s);
-    case 128: return launch_few_d<128>(a, p.few.rows, s);
-    default: return launch_few_d<256>(a, p.few.rows, s);
+    case 64: return launch_few_d<64>(a, p.few.rows, p.few.warps, s);
+    case 128: return launch_few_d<128>(a, p.few.rows, p.few.warps, s);
+    default: return launch_few_d<256>(a, p.few.rows, p.few.warps, s);
     }
 }
 

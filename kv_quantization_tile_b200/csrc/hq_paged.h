@@ -59,6 +59,7 @@ cudaError_t launch_merge(const MergeArgs &a, cudaStream_t s);
 // Where a block's share of the tiles begins (written by the plan kernel).
 struct PagedStart {
     int32_t b, h, rt, tile;  // sequence, KV head, row tile, tile within the job
+    int64_t job;             // the job's first unit of work
 };
 
 struct PagedArgs {
@@ -80,11 +81,12 @@ struct PagedArgs {
     int window;              // positions a query sees, itself included (0: all)
     int row_lo, row_hi;      // sequences with row_lo < q_len * group <= row_hi
     // plan (workspace)
-    int64_t *prefix;         // [batch + 1] tiles before each sequence
+    int64_t *prefix;         // [batch + 1] units of work before each sequence
     PagedStart *start;       // [grid]
     uint32_t *counter;       // [grid] finished parts of the job whose first tile block c holds
     float *part;             // [2 grid] partial results
-    int grid, min_tiles;     // blocks; least tiles a block takes
+    int grid, min_units;     // blocks; least units of work a block takes
+    int job_cost;            // what a job costs beside its tiles, in tiles
     int split, row_tiles;    // clusters (no plan): blocks of a job, row tiles of the longest sequence
     int32_t *status;
 };
@@ -94,6 +96,7 @@ struct PagedShare {
     int grid, rows;                // blocks (0: not launched), rows per row tile
     int row_lo, row_hi;            // the sequences it takes (rows: new tokens x group)
     int split, row_tiles;          // clusters of `split` blocks, one job each (0: planned shares)
+    int warps;                     // consumer warps of a block in a cluster
     uint64_t prefix, start, counter, part;  // offsets
 };
 
@@ -102,7 +105,8 @@ struct PagedPlan {
     uint64_t total;
 };
 
-PagedPlan paged_plan(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_kv, int heads, int group, int head_dim);
+PagedPlan paged_plan(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_kv, int heads, int group, int head_dim,
+                     int64_t window);
 cudaError_t launch_paged(const PagedArgs &a, const PagedPlan &p, int head_dim, void *workspace, cudaStream_t s);
 // The tcgen05 kernel (planned before), and its row tile.
 cudaError_t launch_paged_many(const PagedArgs &a, int head_dim, cudaStream_t s);
@@ -157,43 +161,53 @@ __device__ __forceinline__ void job_tiles(const PagedArgs &a, const Seq &s, int 
     if (n < 1) n = 1;
 }
 
-// The block's walk over its share of the tiles: segments of jobs (sequence,
-// KV head, row tile), in the order sequence, KV head, row tile, tile.
+// The block's walk over its share of the work: segments of jobs (sequence, KV
+// head, row tile), in the order sequence, KV head, row tile, tile.  A job is
+// job_cost units (queries in, results out) and then a unit for each of its
+// tiles; block c takes units total c / grid .. total (c + 1) / grid, of which
+// only tiles count as work to do (a share that begins within a job's own units
+// begins with its first tile).
 template <int T, int RT>
 struct SegWalk {
     Seq s;
     int b, h, rt, nrt;
     int t0, n, lo, hi;    // the job's tiles and cached range
     int first, count;     // the segment: tiles t0 + first .. + count
-    int64_t at, end, total;
     int grid;
+    int64_t job, end, total;  // the job's first unit, the end of the share
 
     __device__ __forceinline__ bool begin(const PagedArgs &a)
     {
         total = a.prefix[a.batch];
-        const int64_t most = (total + a.min_tiles - 1) / a.min_tiles;
+        const int64_t most = (total + a.min_units - 1) / a.min_units;
         grid = (int)min((int64_t)a.grid, most);
         const int c = blockIdx.x;
         if (c >= grid) return false;
-        at = total * c / grid;
         end = total * (c + 1) / grid;
         const PagedStart st = a.start[c];
         b = st.b;
         h = st.h;
         rt = st.rt;
         first = st.tile;
+        job = st.job;
         bool bad;
         s = load_seq(a, b, bad);
         nrt = (s.rows + RT - 1) / RT;
         job_tiles<T, RT>(a, s, rt, t0, n, lo, hi);
-        count = (int)min((int64_t)(n - first), end - at);
-        return true;
+        return cut(a);
+    }
+
+    // the segment's tiles, from `first`
+    __device__ __forceinline__ bool cut(const PagedArgs &a)
+    {
+        count = (int)min((int64_t)(n - first), end - (job + a.job_cost + first));
+        return count > 0;
     }
 
     __device__ __forceinline__ bool next(const PagedArgs &a)
     {
-        at += count;
-        if (at >= end) return false;
+        job += a.job_cost + n;
+        if (job + a.job_cost >= end) return false;
         first = 0;
         if (++rt == nrt) {
             rt = 0;
@@ -208,8 +222,7 @@ struct SegWalk {
             }
         }
         job_tiles<T, RT>(a, s, rt, t0, n, lo, hi);
-        count = (int)min((int64_t)n, end - at);
-        return true;
+        return cut(a);
     }
 
     // Without a plan: a cluster of `split` blocks takes one job, each an equal
@@ -232,10 +245,10 @@ struct SegWalk {
     }
 
     __device__ __forceinline__ bool whole() const { return count == n; }
-    __device__ __forceinline__ int block_of(int64_t g) const { return (int)(((g + 1) * grid - 1) / total); }
-    // blocks that hold a part of this job
-    __device__ __forceinline__ int owner() const { return block_of(at - first); }
-    __device__ __forceinline__ int last() const { return block_of(at - first + n - 1); }
+    __device__ __forceinline__ int block_of(int64_t unit) const { return (int)(((unit + 1) * grid - 1) / total); }
+    // blocks that hold the first and the last tile of this job
+    __device__ __forceinline__ int owner(const PagedArgs &a) const { return block_of(job + a.job_cost); }
+    __device__ __forceinline__ int last(const PagedArgs &a) const { return block_of(job + a.job_cost + n - 1); }
     // a block's parts: one that begins inside a job, one that begins with it
     __device__ __forceinline__ int slot() const { return 2 * (int)blockIdx.x + (first == 0 ? 1 : 0); }
 };
@@ -275,29 +288,48 @@ __device__ __forceinline__ const float *part_of(const PagedArgs &a, int c, int c
     return a.part + (int64_t)(2 * c + (c == c0 ? 1 : 0)) * (RT * (D + 2));
 }
 
-// Join the parts that blocks c0 .. c1 left of row r (packed row pr), columns
-// 4 c .. 4 c + 3, in block order.
-template <int RT, int D>
-__device__ __forceinline__ void join_parts(const PagedArgs &a, int q0, int h, int pr, int r, int c, int c0, int c1)
+// Join the parts that blocks c0 .. c1 left of a job's nr rows (packed rows r0
+// ..), in block order; THREADS threads, N groups of 4 columns each at once to
+// keep their loads in flight together.
+template <int RT, int D, int THREADS>
+__device__ __forceinline__ void join_parts(const PagedArgs &a, int q0, int h, int r0, int nr, int tid, int c0, int c1)
 {
-    float mt = -INFINITY;
-#pragma unroll 8
-    for (int k = c0; k <= c1; k++) mt = fmaxf(mt, __ldcg(part_of<RT, D>(a, k, c0) + r));
-    const float base = mt == -INFINITY ? 0.0f : mt;
-    float l = 0.0f;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-    for (int k = c0; k <= c1; k++) {
-        const float *p = part_of<RT, D>(a, k, c0);
-        const float f = ex2(__ldcg(p + r) - base);
-        l = fmaf(f, __ldcg(p + RT + r), l);
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p + 2 * RT + r * D + 4 * c));
-        acc.x = fmaf(f, v.x, acc.x);
-        acc.y = fmaf(f, v.y, acc.y);
-        acc.z = fmaf(f, v.z, acc.z);
-        acc.w = fmaf(f, v.w, acc.w);
+    constexpr int N = 4, C4 = D / 4;
+    for (int e0 = tid; e0 < nr * C4; e0 += N * THREADS) {
+        int r[N], c[N];
+        float mt[N], l[N];
+        float4 acc[N];
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const int e = min(e0 + i * THREADS, nr * C4 - 1);  // (past the last: the last again, not written)
+            r[i] = e / C4;
+            c[i] = e % C4;
+            mt[i] = -INFINITY;
+            l[i] = 0.0f;
+            acc[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+#pragma unroll 4
+        for (int k = c0; k <= c1; k++)
+#pragma unroll
+            for (int i = 0; i < N; i++) mt[i] = fmaxf(mt[i], __ldcg(part_of<RT, D>(a, k, c0) + r[i]));
+#pragma unroll 2
+        for (int k = c0; k <= c1; k++) {
+            const float *p = part_of<RT, D>(a, k, c0);
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+                const float f = ex2(__ldcg(p + r[i]) - (mt[i] == -INFINITY ? 0.0f : mt[i]));
+                l[i] = fmaf(f, __ldcg(p + RT + r[i]), l[i]);
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(p + 2 * RT + r[i] * D + 4 * c[i]));
+                acc[i].x = fmaf(f, v.x, acc[i].x);
+                acc[i].y = fmaf(f, v.y, acc[i].y);
+                acc[i].z = fmaf(f, v.z, acc[i].z);
+                acc[i].w = fmaf(f, v.w, acc[i].w);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < N; i++)
+            if (e0 + i * THREADS < nr * C4) finish_row(a, q0, h, r0 + r[i], c[i], acc[i], mt[i], l[i]);
     }
-    finish_row(a, q0, h, pr, c, acc, mt, l);
 }
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

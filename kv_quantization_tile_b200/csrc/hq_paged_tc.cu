@@ -251,35 +251,40 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
         const uint32_t to = tmem + lanes + C::O_COL + (uint32_t)(t * D + hf * (D / 2));  // this half's columns of O
         const int pair = 1 + t * 4 + wl;  // barrier of the two warps of the same rows
         uint32_t g = 0;  // tiles so far
-        // this warp's half of 32 query rows of the segment w stands at
-        auto queries = [&]() {
-            constexpr int CH = D / 16, N = CH;  // chunks per half row, loads per lane
-            const int r0 = w.rt * RT + t * 128;
-            uint4 v[N];
-#pragma unroll
-            for (int i = 0; i < N; i++) {
-                const int e = lane + 32 * i, r = r0 + wl * 32 + e / CH, c = hf * CH + e % CH;
-                v[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (r < w.s.rows && a.q_mode != 2) {
-                    const int j = (int)fast_div((uint32_t)r, a.group_div), gg = r - j * a.group;
-                    v[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q.p) + (w.s.q0 + j) * a.q.ts +
-                                                            (w.h * a.group + gg) * a.q.hs + 8 * c);
+        // This warp's half of 32 query rows of a segment, copied on the side (zeros
+        // past the last row), then handed over.
+        constexpr int CH = D / 16;  // chunks per half row, copies per lane
+        auto copy_queries = [&](const SegWalk<T, RT> &x) {
+#pragma unroll 1
+            for (int e = lane; e < 32 * CH; e += 32) {
+                const int rr = wl * 32 + e / CH, c = hf * CH + e % CH, r = x.rt * RT + t * 128 + rr;
+                const bool valid = r < x.s.rows && a.q_mode != 2;
+                const int j = (int)fast_div((uint32_t)r, a.group_div), gg = r - j * a.group;
+                const uint16_t *q = static_cast<const uint16_t *>(a.q.p);
+                if (valid) q += (x.s.q0 + j) * a.q.ts + (x.h * a.group + gg) * a.q.hs + 8 * c;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sq + t * C::QTILE + swizzled_off(128, rr, c)),
+                             "l"(q), "r"(valid ? 16 : 0) : "memory");
+            }
+        };
+        auto hand_queries = [&]() {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            if (a.q_mode == 1)  // a negative scale: -q
+                for (int e = lane; e < 32 * CH; e += 32) {
+                    const uint32_t at = sq + t * C::QTILE + swizzled_off(128, wl * 32 + e / CH, hf * CH + e % CH);
+                    uint32_t v[4];
+                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at) : "memory");
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v[0] ^ 0x80008000u), "r"(v[1] ^ 0x80008000u),
+                                 "r"(v[2] ^ 0x80008000u), "r"(v[3] ^ 0x80008000u) : "memory");
                 }
-            }
-            const uint32_t flip = a.q_mode == 1 ? 0x80008000u : 0u;
-#pragma unroll
-            for (int i = 0; i < N; i++) {
-                const int e = lane + 32 * i;
-                const uint32_t dst = sq + t * C::QTILE + swizzled_off(128, wl * 32 + e / CH, hf * CH + e % CH);
-                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(v[i].x ^ flip), "r"(v[i].y ^ flip),
-                             "r"(v[i].z ^ flip), "r"(v[i].w ^ flip) : "memory");
-            }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full(t));
         };
         bool more = work;
-        if (more) queries();
+        if (more) {
+            copy_queries(w);
+            hand_queries();
+        }
         while (more) {
             const int r = w.rt * RT + t * 128 + wl * 32 + lane, rows = w.s.rows, q0 = w.s.q0, h = w.h;
             int rlo = 0, rhi = 0;
@@ -287,6 +292,8 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                 const int j = (int)fast_div((uint32_t)r, a.group_div);
                 seen_range(a, w.s, j, j, rlo, rhi);
             }
+            SegWalk<T, RT> after = w;
+            more = after.next(a);  // (its lengths are read while the first scores are computed)
             float m = -INFINITY, l = 0.0f;
             bool ok = true;
             for (int tile = w.first; tile < w.first + w.count; tile++, g++) {
@@ -301,6 +308,9 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                 if (NT == 1 && tile > w.first) ok = wait(o_full(t), (g - 1u) & 1u) && ok;
                 ok = __all_sync(FULL, ok);
                 tc_fence_after();
+                // the last scores are there, so the queries are free: the next
+                // segment's take their place
+                if (tile + 1 == w.first + w.count && more && ok) copy_queries(after);
                 const uint32_t mine = ts + (uint32_t)(hf * (T / 2));  // this half's scores, then its weights
                 const int tok0 = (w.t0 + tile) * T + hf * (T / 2);
                 const bool edge = !__all_sync(FULL, rlo <= tok0 && rhi >= tok0 + T / 2);
@@ -409,11 +419,8 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
             if (named_any(9 + t, 256, !ok)) break;
             tc_fence_after();
             const bool whole = w.whole();
-            const int slot = w.slot(), c0 = w.owner(), c1 = w.last();
-            // the next segment's queries take the place of this one's, whose
-            // products are done: its first scores come while O is written out
-            more = w.next(a);
-            if (more) queries();
+            const int slot = w.slot(), c0 = w.owner(a), c1 = w.last(a);
+            if (more) hand_queries();  // its first scores come while O is written out
             const int rr = wl * 32 + lane;  // row of this MMA tile
             if (hf) s_row[t][rr] = l;
             named_sync(pair, 64);
@@ -485,9 +492,11 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                         return a.part + ((int64_t)(2 * k + (k == c0 ? 1 : 0)) * NT + t) * (128 * (D + 2));
                     };
                     mt = -INFINITY;
+#pragma unroll 4
                     for (int k = c0; k <= c1; k++) mt = fmaxf(mt, __ldcg(part_at(k) + rr));
                     const float from = mt == -INFINITY ? 0.0f : mt;
                     lt = 0.0f;
+#pragma unroll 4
                     for (int k = c0; k <= c1; k++) lt = fmaf(ex2(__ldcg(part_at(k) + rr) - from), __ldcg(part_at(k) + 128 + rr), lt);
                     const float f = lt == 0.0f ? 0.0f : 1.0f / lt;
 #pragma unroll 1
@@ -495,17 +504,20 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                         float v[32];
 #pragma unroll
                         for (int i = 0; i < 32; i++) v[i] = 0.0f;
-#pragma unroll 2
-                        for (int k = c0; k <= c1; k++) {
-                            const float e = ex2(__ldcg(part_at(k) + rr) - from);
-                            const float4 *p = reinterpret_cast<const float4 *>(part_at(k) + 256) + (hf * (D / 8) + 8 * c) * 128 + rr;
+#pragma unroll 1
+                        for (int k = c0; k <= c1; k += 2) {  // two parts' loads in flight
+                            const bool two = k < c1;
+                            const float e0 = ex2(__ldcg(part_at(k) + rr) - from), e1 = two ? ex2(__ldcg(part_at(k + 1) + rr) - from) : 0.0f;
+                            const float4 *p0 = reinterpret_cast<const float4 *>(part_at(k) + 256) + (hf * (D / 8) + 8 * c) * 128 + rr;
+                            const float4 *p1 = reinterpret_cast<const float4 *>(part_at(k + 1) + 256) + (hf * (D / 8) + 8 * c) * 128 + rr;
 #pragma unroll
                             for (int i = 0; i < 8; i++) {
-                                const float4 x = __ldcg(p + i * 128);
-                                v[4 * i] = fmaf(e, x.x, v[4 * i]);
-                                v[4 * i + 1] = fmaf(e, x.y, v[4 * i + 1]);
-                                v[4 * i + 2] = fmaf(e, x.z, v[4 * i + 2]);
-                                v[4 * i + 3] = fmaf(e, x.w, v[4 * i + 3]);
+                                const float4 x = __ldcg(p0 + i * 128);
+                                const float4 y = two ? __ldcg(p1 + i * 128) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                                v[4 * i] = fmaf(e1, y.x, fmaf(e0, x.x, v[4 * i]));
+                                v[4 * i + 1] = fmaf(e1, y.y, fmaf(e0, x.y, v[4 * i + 1]));
+                                v[4 * i + 2] = fmaf(e1, y.z, fmaf(e0, x.z, v[4 * i + 2]));
+                                v[4 * i + 3] = fmaf(e1, y.w, fmaf(e0, x.w, v[4 * i + 3]));
                             }
                         }
                         put(c, v, f, lt == 0.0f);
@@ -514,6 +526,7 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
             }
             if (write && hf == 0 && a.lse && r < rows)
                 a.lse[tok * (a.heads * a.group) + head] = lt == 0.0f ? -INFINITY : fmaf(mt, 0.693147180559945309f, logf(lt));
+            w = after;
         }
     } else {
         if ((warp & 3) == 0) {

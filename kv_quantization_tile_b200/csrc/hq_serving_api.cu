@@ -233,7 +233,8 @@ int hq_paged_attention_workspace_bytes(int64_t batch, int64_t tokens, int64_t ma
     if (!out) return HQ_ERR_ARG;
     const int rc = check_paged_sizes(batch, tokens, max_q, max_kv, heads, head_dim, group);
     if (rc) return rc;
-    *out = paged_plan(batch, tokens, max_q, max_kv, heads, group, head_dim).total;
+    // a window only ever needs less
+    *out = paged_plan(batch, tokens, max_q, max_kv, heads, group, head_dim, 0).total;
     return HQ_OK;
 }
 
@@ -254,7 +255,7 @@ int hq_paged_attention(const hq_rows *q, const int32_t *q_start, const int32_t *
     if (!readable(q, tokens, heads) || q->dtype != HQ_BF16 || !writable(out, tokens, heads, d)) return HQ_ERR_ARG;
     if (!q_start || !kv_len || !aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(lse, 4)) return HQ_ERR_ARG;
     if (table_width > 0 && (!table || !aligned(table, 4))) return HQ_ERR_ARG;
-    const PagedPlan p = paged_plan(batch, tokens, max_q, max_kv, pages->heads, group, d);
+    const PagedPlan p = paged_plan(batch, tokens, max_q, max_kv, pages->heads, group, d, window);
     if (!workspace || !aligned(workspace, 16) || workspace_bytes < p.total) return HQ_ERR_WORKSPACE;
     PagedArgs a{};
     a.q = rows_of(q, tokens, heads);
