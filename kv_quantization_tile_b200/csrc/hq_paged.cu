@@ -18,10 +18,10 @@ namespace hq {
 
 namespace {
 
-constexpr int kFewT = 64;          // tokens per tile of the planned kernel
+constexpr int kFewT = 64;          // tokens per tile
 constexpr int kPlanThreads = 1024;
 // A job's own cost in tiles (prologue and results), for equal shares
-constexpr int kJobCostFew = 2, kJobCostMany = 2;
+constexpr int kJobCostFew = 2, kJobCostMany = 5;
 constexpr int kClusterTiles = 16;  // most tiles a block takes of an uneven batch without a plan
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4])
@@ -45,14 +45,14 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 template <int THREADS>
 __device__ __forceinline__ void named_sync1() { asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory"); }
 
-// W consumer warps and one that loads; tiles of 16 W tokens; a row tile of 16 WM rows
-template <int D, int WM, int W>
+// Four consumer warps and one that loads; a row tile of 16 WM rows
+template <int D, int WM>
 struct Few {
-    static constexpr int T = 16 * W, RT = 16 * WM, ROWS = 32 * W, THREADS = ROWS + 32;
+    static constexpr int T = kFewT, RT = 16 * WM, ROWS = 128, THREADS = ROWS + 32;
     // stages of K and V tiles: about 64 KB in flight per SM keep HBM busy
     static constexpr int STAGES = D == 64 ? 4 : 3;
     // blocks per SM that shared memory and registers allow
-    static constexpr int BLOCKS = W > 4 ? 1 : D == 64 ? 3 : D == 128 ? 2 : 1;
+    static constexpr int BLOCKS = D == 64 ? 3 : D == 128 ? 2 : 1;
     static constexpr uint32_t TILE = T * D * 2;
     static constexpr size_t SMEM = 1024 + (D == 256 ? RT * D * 2 : 0) + (size_t)STAGES * 2 * TILE;
 };
@@ -167,9 +167,9 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedArg
 }
 
 // ------------------------------------------------------------ few rows
-// W consumer warps; a row tile has 16 WM rows.  Warp (wm, wn) multiplies rows
+// Four consumer warps; a row tile has 16 WM rows.  Warp (wm, wn) multiplies rows
 // 16 wm .. with its share of each tile's tokens and keeps its own running
-// softmax; the W / WM warps of the same rows are joined after the last tile.  One
+// softmax; the 4 / WM warps of the same rows are joined after the last tile.  One
 // more warp copies the tiles' pages with TMA into a ring of stages, so the
 // consumers meet no one else between tiles: each waits for a stage's bytes and
 // reports when it has read them.  (With the tiles copied by the consumers
@@ -177,13 +177,13 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedArg
 // clocks, most of them addresses and waiting.)
 // CLUSTER: no plan; the blocks of a cluster share one job, and join their
 // results through each other's shared memory.
-template <int D, int WM, int W, bool CLUSTER>
-__global__ void __launch_bounds__(Few<D, WM, W>::THREADS, Few<D, WM, W>::BLOCKS)
+template <int D, int WM, bool CLUSTER>
+__global__ void __launch_bounds__(Few<D, WM>::THREADS, Few<D, WM>::BLOCKS)
 paged_few_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
 {
-    using F = Few<D, WM, W>;
+    using F = Few<D, WM>;
     constexpr int T = F::T, RT = F::RT, ROWS = F::ROWS, STAGES = F::STAGES, KS = D / 16;
-    constexpr int WN = W / WM, NC = T / WN / 16;  // NC: 16-token chunks per warp and tile
+    constexpr int W = 4, WN = W / WM, NC = T / WN / 16;  // NC: 16-token chunks per warp and tile
     constexpr uint32_t TILE = F::TILE;
     constexpr bool QREG = D <= 128;  // q fragments stay in registers
     extern __shared__ uint8_t raw[];
@@ -203,6 +203,10 @@ paged_few_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, co
             mbar_init(empty(s), W);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == W && lane == 0) {
+        prefetch_map(&kmap);
+        prefetch_map(&vmap);
     }
     SegWalk<T, RT> w;
     bool work;
@@ -609,13 +613,13 @@ __global__ void __launch_bounds__(256) merge_kernel(const MergeArgs a)
 // ------------------------------------------------------------ launch
 namespace {
 
-template <int D, int WM, int W, bool CLUSTER>
+template <int D, int WM, bool CLUSTER>
 cudaError_t launch_few(const PagedArgs &a, cudaStream_t s)
 {
-    using F = Few<D, WM, W>;
+    using F = Few<D, WM>;
     CUtensorMap kmap, vmap;
     const int box = (1 << a.page_shift) < F::T ? 1 << a.page_shift : F::T;
-    const auto kern = paged_few_kernel<D, WM, W, CLUSTER>;
+    const auto kern = paged_few_kernel<D, WM, CLUSTER>;
     cudaError_t e = page_map(&kmap, a, a.k, D, box);
     if (e == cudaSuccess) e = page_map(&vmap, a, a.v, D, box);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)F::SMEM);
@@ -626,22 +630,14 @@ cudaError_t launch_few(const PagedArgs &a, cudaStream_t s)
     return launch_dependent(kern, a.grid, F::THREADS, F::SMEM, s, a, kmap, vmap);
 }
 
-template <int D, int WM>
-cudaError_t launch_few_m(const PagedArgs &a, int warps, cudaStream_t s)
-{
-    if (!a.split) return launch_few<D, WM, 4, false>(a, s);
-    if constexpr (WM == 1 && D <= 128)
-        if (warps == 8) return launch_few<D, WM, 8, true>(a, s);
-    return launch_few<D, WM, 4, true>(a, s);
-}
-
 template <int D>
-cudaError_t launch_few_d(const PagedArgs &a, int rows, int warps, cudaStream_t s)
+cudaError_t launch_few_d(const PagedArgs &a, int rows, cudaStream_t s)
 {
+    const bool c = a.split > 0;
     switch (rows) {
-    case 16: return launch_few_m<D, 1>(a, warps, s);
-    case 32: return launch_few_m<D, 2>(a, warps, s);
-    default: return launch_few_m<D, 4>(a, warps, s);
+    case 16: return c ? launch_few<D, 1, true>(a, s) : launch_few<D, 1, false>(a, s);
+    case 32: return c ? launch_few<D, 2, true>(a, s) : launch_few<D, 2, false>(a, s);
+    default: return c ? launch_few<D, 4, true>(a, s) : launch_few<D, 4, false>(a, s);
     }
 }
 
@@ -697,24 +693,24 @@ PagedPlan paged_plan(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_k
         p.few.grid = sm_count() * (head_dim == 64 ? 3 : head_dim == 128 ? 2 : 1);
         // One launch in clusters where the blocks of all jobs fit at once and
         // uneven lengths cannot make one cluster late: a single sequence (its
-        // jobs are alike), or few tiles per block.
-        // At one block per SM the block has eight consumer warps (16 rows, head_dim
-        // up to 128): four leave a tile's chain of dependent steps exposed.
+        // jobs are alike), or few tiles per block.  Clusters of 16 fill a GPC, of
+        // which there are eight: not for more jobs.  Measured (8 KV heads of 128,
+        // one sequence of 4096 / 32768): 11.1 / 32.8 us, by shares 16.4 / 47.2.
         const int64_t row_tiles = (rows + p.few.rows - 1) / p.few.rows;
         const int64_t reach = window > 0 && window + max_q < max_kv ? window + max_q : max_kv;  // tokens a job reads
         const int64_t tiles = (reach + kFewT - 1) / kFewT + (reach < max_kv ? 1 : 0);
-        const int64_t jobs = batch * heads * row_tiles;
+        const int64_t jobs = batch * heads * row_tiles, most = jobs <= 8 ? 16 : 8;
         if (!many && jobs > 0 && jobs <= p.few.grid) {
             int split = 1;
-            while (split < 16 && 2 * split * jobs <= p.few.grid && split < tiles) split *= 2;
-            const int64_t per_block = (tiles + split - 1) / split;
-            if (per_block <= kClusterTiles || (batch == 1 && 2 * split * jobs >= sm_count())) {
+            while (split < most && 2 * split * jobs <= p.few.grid && split < tiles) split *= 2;
+            if ((tiles + split - 1) / split <= kClusterTiles || (batch == 1 && jobs <= 16)) {
                 p.few.split = split;
                 p.few.row_tiles = (int)row_tiles;
                 p.few.grid = (int)(jobs * split);
-                p.few.warps = p.few.rows == 16 && head_dim <= 128 && p.few.grid <= sm_count() && per_block >= 4 ? 8 : 4;
             }
         }
+        // by shares: at most 32 parts of a job on average, which one block joins
+        if (!many && !p.few.split && 32 * jobs < p.few.grid) p.few.grid = (int)(32 * jobs > 0 ? 32 * jobs : 1);
         if (!p.few.split) place(p.few, 1);
     }
     if (many) {
@@ -760,9 +756,9 @@ cudaError_t launch_paged(const PagedArgs &args, const PagedPlan &p, int head_dim
     }
     if (e != cudaSuccess) return e;
     switch (head_dim) {
-    case 64: return launch_few_d<64>(a, p.few.rows, p.few.warps, s);
-    case 128: return launch_few_d<128>(a, p.few.rows, p.few.warps, s);
-    default: return launch_few_d<256>(a, p.few.rows, p.few.warps, s);
+    case 64: return launch_few_d<64>(a, p.few.rows, s);
+    case 128: return launch_few_d<128>(a, p.few.rows, s);
+    default: return launch_few_d<256>(a, p.few.rows, s);
     }
 }
 

@@ -96,7 +96,6 @@ struct PagedShare {
     int grid, rows;                // blocks (0: not launched), rows per row tile
     int row_lo, row_hi;            // the sequences it takes (rows: new tokens x group)
     int split, row_tiles;          // clusters of `split` blocks, one job each (0: planned shares)
-    int warps;                     // consumer warps of a block in a cluster
     uint64_t prefix, start, counter, part;  // offsets
 };
 
@@ -289,12 +288,12 @@ __device__ __forceinline__ const float *part_of(const PagedArgs &a, int c, int c
 }
 
 // Join the parts that blocks c0 .. c1 left of a job's nr rows (packed rows r0
-// ..), in block order; THREADS threads, N groups of 4 columns each at once to
-// keep their loads in flight together.
-template <int RT, int D, int THREADS>
-__device__ __forceinline__ void join_parts(const PagedArgs &a, int q0, int h, int r0, int nr, int tid, int c0, int c1)
+// ..), in block order, G parts' loads in flight: a thread takes N groups of 4
+// columns at once.
+template <int RT, int D, int THREADS, int N, int G>
+__device__ __forceinline__ void join_some(const PagedArgs &a, int q0, int h, int r0, int nr, int tid, int c0, int c1)
 {
-    constexpr int N = 4, C4 = D / 4;
+    constexpr int C4 = D / 4;
     for (int e0 = tid; e0 < nr * C4; e0 += N * THREADS) {
         int r[N], c[N];
         float mt[N], l[N];
@@ -308,28 +307,54 @@ __device__ __forceinline__ void join_parts(const PagedArgs &a, int q0, int h, in
             l[i] = 0.0f;
             acc[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
-#pragma unroll 4
-        for (int k = c0; k <= c1; k++)
+        for (int k = c0; k <= c1; k += G) {
+            float m[G][N], s[G][N];
+            float4 v[G][N];
 #pragma unroll
-            for (int i = 0; i < N; i++) mt[i] = fmaxf(mt[i], __ldcg(part_of<RT, D>(a, k, c0) + r[i]));
-#pragma unroll 2
-        for (int k = c0; k <= c1; k++) {
-            const float *p = part_of<RT, D>(a, k, c0);
+            for (int g = 0; g < G; g++)
+#pragma unroll
+                for (int i = 0; i < N; i++) {
+                    m[g][i] = -INFINITY;
+                    s[g][i] = 0.0f;
+                    v[g][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (k + g <= c1) {
+                        const float *p = part_of<RT, D>(a, k + g, c0);
+                        m[g][i] = __ldcg(p + r[i]);
+                        s[g][i] = __ldcg(p + RT + r[i]);
+                        v[g][i] = __ldcg(reinterpret_cast<const float4 *>(p + 2 * RT + r[i] * D + 4 * c[i]));
+                    }
+                }
 #pragma unroll
             for (int i = 0; i < N; i++) {
-                const float f = ex2(__ldcg(p + r[i]) - (mt[i] == -INFINITY ? 0.0f : mt[i]));
-                l[i] = fmaf(f, __ldcg(p + RT + r[i]), l[i]);
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(p + 2 * RT + r[i] * D + 4 * c[i]));
-                acc[i].x = fmaf(f, v.x, acc[i].x);
-                acc[i].y = fmaf(f, v.y, acc[i].y);
-                acc[i].z = fmaf(f, v.z, acc[i].z);
-                acc[i].w = fmaf(f, v.w, acc[i].w);
+                float top = mt[i];
+#pragma unroll
+                for (int g = 0; g < G; g++) top = fmaxf(top, m[g][i]);
+                const float base = top == -INFINITY ? 0.0f : top, f = ex2(mt[i] - base);
+                mt[i] = top;
+                l[i] *= f;
+                acc[i] = make_float4(acc[i].x * f, acc[i].y * f, acc[i].z * f, acc[i].w * f);
+#pragma unroll
+                for (int g = 0; g < G; g++) {
+                    const float w = ex2(m[g][i] - base);
+                    l[i] = fmaf(w, s[g][i], l[i]);
+                    acc[i].x = fmaf(w, v[g][i].x, acc[i].x);
+                    acc[i].y = fmaf(w, v[g][i].y, acc[i].y);
+                    acc[i].z = fmaf(w, v[g][i].z, acc[i].z);
+                    acc[i].w = fmaf(w, v[g][i].w, acc[i].w);
+                }
             }
         }
 #pragma unroll
         for (int i = 0; i < N; i++)
             if (e0 + i * THREADS < nr * C4) finish_row(a, q0, h, r0 + r[i], c[i], acc[i], mt[i], l[i]);
     }
+}
+
+template <int RT, int D, int THREADS>
+__device__ __forceinline__ void join_parts(const PagedArgs &a, int q0, int h, int r0, int nr, int tid, int c0, int c1)
+{
+    if (nr * (D / 4) <= THREADS) join_some<RT, D, THREADS, 1, 8>(a, q0, h, r0, nr, tid, c0, c1);
+    else join_some<RT, D, THREADS, 4, 2>(a, q0, h, r0, nr, tid, c0, c1);
 }
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

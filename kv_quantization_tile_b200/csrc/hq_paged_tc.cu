@@ -240,6 +240,10 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
         return false;
     };
 
+    if (warp == 2 && lane == 0) {
+        prefetch_map(&kmap);
+        prefetch_map(&vmap);
+    }
     pdl_wait();
     SegWalk<T, RT> w;
     const bool work = w.begin(a);
