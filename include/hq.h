@@ -528,8 +528,8 @@ int hq_paged_attention(const hq_rows *q, const int32_t *q_start, const int32_t *
  *   lse = log(exp(lse_a) + exp(lse_b))
  * a, b, out  [tokens][heads][head_dim], each HQ_BF16 or HQ_F32, head_dim a
  *            multiple of 8 up to 1024; lse_a, lse_b, lse fp32 [tokens][heads]
- *            (lse may be NULL).  A part whose lse is minus infinity is not
- *            read; if both are, the row is zero.  out may be a or b themselves
+ *            (lse may be NULL).  A part whose lse is minus infinity counts
+ *            for nothing, whatever it holds; if both are, the row is zero.  out may be a or b themselves
  *            (same strides and type); lse must be neither lse_a nor lse_b
  *            (HQ_ERR_ARG: other threads still read them).
  * tokens * heads < 2^32. */

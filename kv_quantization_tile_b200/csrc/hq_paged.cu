@@ -22,7 +22,7 @@ constexpr int kFewT = 64;          // tokens per tile
 constexpr int kPlanThreads = 1024;
 // A job's own cost in tiles (prologue and results), for equal shares
 constexpr int kJobCostFew = 2, kJobCostMany = 5;
-constexpr int kClusterTiles = 16;  // most tiles a block takes of an uneven batch without a plan
+constexpr int kClusterTiles = 32;  // most tiles a block takes of an uneven batch without a plan
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4])
 {
@@ -498,28 +498,12 @@ paged_few_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, co
         if constexpr (CLUSTER) {
             const int rank = (int)blockIdx.x % a.split;
             cluster_sync();
-            for (int e = rank * ROWS + tid; e < nr * C4; e += a.split * ROWS) {
-                const int r = e / C4, c = e % C4;
-                const uint32_t am = smem_u32(s_fm + r), al = smem_u32(s_fl + r),
-                               ao = smem_u32(so + r * D + ((4 * c) ^ ((r & 7) << 3)));
-                float mt = -INFINITY;
-#pragma unroll 8
-                for (int k = 0; k < a.split; k++) mt = fmaxf(mt, cluster_ld(cluster_map(am, k)));
-                const float bs = mt == -INFINITY ? 0.0f : mt;
-                float lt = 0.0f;
-                float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-                for (int k = 0; k < a.split; k++) {
-                    const float f = ex2(cluster_ld(cluster_map(am, k)) - bs);
-                    lt = fmaf(f, cluster_ld(cluster_map(al, k)), lt);
-                    const float4 v = cluster_ld4(cluster_map(ao, k));
-                    acc.x = fmaf(f, v.x, acc.x);
-                    acc.y = fmaf(f, v.y, acc.y);
-                    acc.z = fmaf(f, v.z, acc.z);
-                    acc.w = fmaf(f, v.w, acc.w);
-                }
-                finish_row(a, w.s.q0, w.h, r0 + r, c, acc, mt, lt);
-            }
+            auto load = [&](int k, int r, int c, float &m, float &l, float4 &v) {
+                m = cluster_ld(cluster_map(smem_u32(s_fm + r), k));
+                l = cluster_ld(cluster_map(smem_u32(s_fl + r), k));
+                v = cluster_ld4(cluster_map(smem_u32(so + r * D + ((4 * c) ^ ((r & 7) << 3))), k));
+            };
+            join_some<D, 1, 8>(a, w.s.q0, w.h, r0, nr, rank * ROWS + tid, a.split * ROWS, 0, a.split - 1, load);
         } else if (!whole) {
             __threadfence();
             named_sync1<ROWS>();
@@ -528,7 +512,14 @@ paged_few_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, co
             named_sync1<ROWS>();
             if (s_last) {
                 __threadfence();
-                join_parts<RT, D, ROWS>(a, w.s.q0, w.h, r0, nr, tid, c0, c1);
+                auto load = [&](int k, int r, int c, float &m, float &l, float4 &v) {
+                    const float *p = part_of<RT, D>(a, k, c0);
+                    m = __ldcg(p + r);
+                    l = __ldcg(p + RT + r);
+                    v = __ldcg(reinterpret_cast<const float4 *>(p + 2 * RT + r * D + 4 * c));
+                };
+                if (nr * C4 <= ROWS) join_some<D, 1, 8>(a, w.s.q0, w.h, r0, nr, tid, ROWS, c0, c1, load);
+                else join_some<D, 4, 2>(a, w.s.q0, w.h, r0, nr, tid, ROWS, c0, c1, load);
             }
         }
         if constexpr (!CLUSTER) {
@@ -547,24 +538,36 @@ paged_few_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, co
 // ------------------------------------------------------------ join
 namespace {
 
-__device__ __forceinline__ void load8(const Rows &r, int64_t tok, int64_t h, int u, bool used, float (&v)[8])
+// 8 elements as they lie: 32 bytes of binary32, 16 of bf16
+struct Raw8 {
+    uint4 a, b;
+};
+
+__device__ __forceinline__ Raw8 load_raw(const Rows &r, int64_t tok, int64_t h, int u)
 {
     const int64_t off = tok * r.ts + h * r.hs + 8 * u;
-#pragma unroll
-    for (int i = 0; i < 8; i++) v[i] = 0.0f;
-    if (!used) return;
+    Raw8 x;
     if (r.f32) {
-        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(r.p) + off);
-        const float4 x = p[0], y = p[1];
-        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-        v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(r.p) + off);
+        x.a = p[0];
+        x.b = p[1];
     } else {
-        const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(r.p) + off);
-        const uint32_t ww[4] = { w.x, w.y, w.z, w.w };
+        x.a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(r.p) + off);
+    }
+    return x;
+}
+
+__device__ __forceinline__ void as_float(const Rows &r, const Raw8 &x, float (&v)[8])
+{
+    const uint32_t a[4] = { x.a.x, x.a.y, x.a.z, x.a.w }, b[4] = { x.b.x, x.b.y, x.b.z, x.b.w };
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            v[2 * i] = __uint_as_float(ww[i] << 16);
-            v[2 * i + 1] = __uint_as_float(ww[i] & 0xffff0000u);
+    for (int i = 0; i < 4; i++) {
+        if (r.f32) {
+            v[i] = __uint_as_float(a[i]);
+            v[4 + i] = __uint_as_float(b[i]);
+        } else {
+            v[2 * i] = __uint_as_float(a[i] << 16);
+            v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
         }
     }
 }
@@ -584,29 +587,51 @@ __device__ __forceinline__ void store8(const Rows &r, int64_t tok, int64_t h, in
 
 }  // namespace
 
-// out = (wa a + wb b) / (wa + wb), w = exp(lse - max), 8 elements per thread.
-// A part that saw nothing (lse -inf) has weight 0 and its row is not used,
-// whatever it holds.  HBM-bound: three rows per (token, head).
+// out = (wa a + wb b) / (wa + wb), w = exp(lse - max).  A part that saw nothing
+// (lse -inf) has weight 0 and what its row holds is not used.  HBM-bound: three
+// rows per (token, head).  A thread takes the same 8 elements of kMergeRows rows
+// at once, all loads ahead of the first use (one row at a time, its loads after
+// its lse: 37 us for 4099 x 32 x 128, two bf16 parts and a binary32 result).
+constexpr int kMergeRows = 4;
+
 __global__ void __launch_bounds__(256) merge_kernel(const MergeArgs a)
 {
-    const int units = a.head_dim / 8;
-    const int64_t n = a.tokens * a.heads * units;
-    for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < n; e += (int64_t)gridDim.x * blockDim.x) {
-        const uint32_t row = (uint32_t)(e / units);
-        const int u = (int)(e - (int64_t)row * units);
-        const uint32_t tok = fast_div(row, a.heads_div), h = row - tok * (uint32_t)a.heads;
-        const float la = a.lse_a[row], lb = a.lse_b[row];
-        const float top = (la != la || lb != lb) ? la + lb : fmaxf(la, lb);
-        const float ea = la == -INFINITY ? 0.0f : expf(la - top), eb = lb == -INFINITY ? 0.0f : expf(lb - top);
-        const float sum = ea + eb;
-        const float wa = ea == 0.0f ? 0.0f : ea / sum, wb = eb == 0.0f ? 0.0f : eb / sum;
-        float x[8], y[8];
-        load8(a.a, tok, h, u, la != -INFINITY, x);
-        load8(a.b, tok, h, u, lb != -INFINITY, y);
+    const int units = a.head_dim / 8, per = 256 / units;  // units of a row, rows of a block's pass
+    const int lr = (int)threadIdx.x / units, u = (int)threadIdx.x - lr * units;
+    if (lr >= per) return;
+    const int64_t rows = a.tokens * a.heads;
+    for (int64_t r0 = (int64_t)blockIdx.x * per * kMergeRows + lr; r0 < rows; r0 += (int64_t)gridDim.x * per * kMergeRows) {
+        float la[kMergeRows], lb[kMergeRows];
+        Raw8 x[kMergeRows], y[kMergeRows];
+        uint32_t tok[kMergeRows], h[kMergeRows];
 #pragma unroll
-        for (int i = 0; i < 8; i++) x[i] = wa * x[i] + wb * y[i];
-        store8(a.out, tok, h, u, x);
-        if (u == 0 && a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : top + logf(sum);
+        for (int i = 0; i < kMergeRows; i++) {
+            const int64_t row = r0 + (int64_t)i * per;
+            if (row >= rows) break;
+            tok[i] = fast_div((uint32_t)row, a.heads_div);
+            h[i] = (uint32_t)row - tok[i] * (uint32_t)a.heads;
+            la[i] = a.lse_a[row];
+            lb[i] = a.lse_b[row];
+            x[i] = load_raw(a.a, tok[i], h[i], u);
+            y[i] = load_raw(a.b, tok[i], h[i], u);
+        }
+#pragma unroll
+        for (int i = 0; i < kMergeRows; i++) {
+            const int64_t row = r0 + (int64_t)i * per;
+            if (row >= rows) break;
+            const float top = (la[i] != la[i] || lb[i] != lb[i]) ? la[i] + lb[i] : fmaxf(la[i], lb[i]);
+            const float ea = la[i] == -INFINITY ? 0.0f : expf(la[i] - top), eb = lb[i] == -INFINITY ? 0.0f : expf(lb[i] - top);
+            const float sum = ea + eb;
+            const float wa = ea == 0.0f ? 0.0f : ea / sum, wb = eb == 0.0f ? 0.0f : eb / sum;
+            float v[8], z[8];
+            as_float(a.a, x[i], v);
+            as_float(a.b, y[i], z);
+#pragma unroll
+            for (int k = 0; k < 8; k++)
+                v[k] = wa * (la[i] == -INFINITY ? 0.0f : v[k]) + wb * (lb[i] == -INFINITY ? 0.0f : z[k]);
+            store8(a.out, tok[i], h[i], u, v);
+            if (u == 0 && a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : top + logf(sum);
+        }
     }
 }
 
@@ -694,12 +719,14 @@ PagedPlan paged_plan(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_k
         // One launch in clusters where the blocks of all jobs fit at once and
         // uneven lengths cannot make one cluster late: a single sequence (its
         // jobs are alike), or few tiles per block.  Clusters of 16 fill a GPC, of
-        // which there are eight: not for more jobs.  Measured (8 KV heads of 128,
-        // one sequence of 4096 / 32768): 11.1 / 32.8 us, by shares 16.4 / 47.2.
+        // which there are eight (half of them, where an SM holds one block): not
+        // for more jobs.  Measured, 8 KV heads of 128: one sequence of 4096 / 32768
+        // tokens 10.3 / 32.8 us, by shares 16.4 / 47.2; eight of 4096 to 8192
+        // tokens 40.6 us, by shares 48.7.
         const int64_t row_tiles = (rows + p.few.rows - 1) / p.few.rows;
         const int64_t reach = window > 0 && window + max_q < max_kv ? window + max_q : max_kv;  // tokens a job reads
         const int64_t tiles = (reach + kFewT - 1) / kFewT + (reach < max_kv ? 1 : 0);
-        const int64_t jobs = batch * heads * row_tiles, most = jobs <= 8 ? 16 : 8;
+        const int64_t jobs = batch * heads * row_tiles, most = jobs <= (head_dim == 256 ? 4 : 8) ? 16 : 8;
         if (!many && jobs > 0 && jobs <= p.few.grid) {
             int split = 1;
             while (split < most && 2 * split * jobs <= p.few.grid && split < tiles) split *= 2;
@@ -766,9 +793,8 @@ cudaError_t launch_merge(const MergeArgs &args, cudaStream_t s)
 {
     MergeArgs a = args;
     a.heads_div = make_fastdiv((uint32_t)a.heads);
-    const int64_t n = a.tokens * a.heads * (a.head_dim / 8);
-    const int64_t blocks = (n + 255) / 256;
-    const int64_t most = (int64_t)sm_count() * 8;
+    const int64_t per = 256 / (a.head_dim / 8) * kMergeRows, rows = a.tokens * a.heads;
+    const int64_t blocks = (rows + per - 1) / per, most = (int64_t)sm_count() * 16;
     merge_kernel<<<(unsigned)(blocks < most ? blocks : most), 256, 0, s>>>(a);
     return cudaGetLastError();
 }

@@ -287,27 +287,29 @@ __device__ __forceinline__ const float *part_of(const PagedArgs &a, int c, int c
     return a.part + (int64_t)(2 * c + (c == c0 ? 1 : 0)) * (RT * (D + 2));
 }
 
-// Join the parts that blocks c0 .. c1 left of a job's nr rows (packed rows r0
-// ..), in block order, G parts' loads in flight: a thread takes N groups of 4
-// columns at once.
-template <int RT, int D, int THREADS, int N, int G>
-__device__ __forceinline__ void join_some(const PagedArgs &a, int q0, int h, int r0, int nr, int tid, int c0, int c1)
+// Join parts k0 .. k1 of a job's nr rows (packed rows r0 ..) in order: load(k, r,
+// c, m, l, v) gives part k's maximum, weight sum and columns 4 c .. of row r.
+// Thread e0 of `threads` takes N groups of 4 columns at once, G parts' loads in
+// flight.
+template <int D, int N, int G, typename F>
+__device__ __forceinline__ void join_some(const PagedArgs &a, int q0, int h, int r0, int nr, int e0, int threads, int k0, int k1,
+                                          F load)
 {
     constexpr int C4 = D / 4;
-    for (int e0 = tid; e0 < nr * C4; e0 += N * THREADS) {
+    for (; e0 < nr * C4; e0 += N * threads) {
         int r[N], c[N];
         float mt[N], l[N];
         float4 acc[N];
 #pragma unroll
         for (int i = 0; i < N; i++) {
-            const int e = min(e0 + i * THREADS, nr * C4 - 1);  // (past the last: the last again, not written)
+            const int e = min(e0 + i * threads, nr * C4 - 1);  // (past the last: the last again, not written)
             r[i] = e / C4;
             c[i] = e % C4;
             mt[i] = -INFINITY;
             l[i] = 0.0f;
             acc[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
-        for (int k = c0; k <= c1; k += G) {
+        for (int k = k0; k <= k1; k += G) {
             float m[G][N], s[G][N];
             float4 v[G][N];
 #pragma unroll
@@ -317,12 +319,7 @@ __device__ __forceinline__ void join_some(const PagedArgs &a, int q0, int h, int
                     m[g][i] = -INFINITY;
                     s[g][i] = 0.0f;
                     v[g][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (k + g <= c1) {
-                        const float *p = part_of<RT, D>(a, k + g, c0);
-                        m[g][i] = __ldcg(p + r[i]);
-                        s[g][i] = __ldcg(p + RT + r[i]);
-                        v[g][i] = __ldcg(reinterpret_cast<const float4 *>(p + 2 * RT + r[i] * D + 4 * c[i]));
-                    }
+                    if (k + g <= k1) load(k + g, r[i], c[i], m[g][i], s[g][i], v[g][i]);
                 }
 #pragma unroll
             for (int i = 0; i < N; i++) {
@@ -346,15 +343,8 @@ __device__ __forceinline__ void join_some(const PagedArgs &a, int q0, int h, int
         }
 #pragma unroll
         for (int i = 0; i < N; i++)
-            if (e0 + i * THREADS < nr * C4) finish_row(a, q0, h, r0 + r[i], c[i], acc[i], mt[i], l[i]);
+            if (e0 + i * threads < nr * C4) finish_row(a, q0, h, r0 + r[i], c[i], acc[i], mt[i], l[i]);
     }
-}
-
-template <int RT, int D, int THREADS>
-__device__ __forceinline__ void join_parts(const PagedArgs &a, int q0, int h, int r0, int nr, int tid, int c0, int c1)
-{
-    if (nr * (D / 4) <= THREADS) join_some<RT, D, THREADS, 1, 8>(a, q0, h, r0, nr, tid, c0, c1);
-    else join_some<RT, D, THREADS, 4, 2>(a, q0, h, r0, nr, tid, c0, c1);
 }
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
