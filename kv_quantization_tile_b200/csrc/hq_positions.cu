@@ -13,8 +13,13 @@
 //
 // Bound by HBM: every element is read and written once.  A block turns a few
 // tokens: it computes each token's rotary / 2 cosines and sines once into
-// shared memory, then every thread moves 16 elements of one head at a time
-// (two 8-element units, 16-byte accesses), all heads of q, k and v alike.
+// shared memory, then every thread moves 16 elements of one head at a time, all
+// heads of q, k and v alike.  The 16 are four quads of 4 elements so placed
+// that a warp's stores are contiguous: pairs of adjacent quads, 16 bytes, where
+// the output is bf16; quads on their own, 16 bytes, where it is binary32 (8191 x
+// 32 x 128 in binary32: 45.7 us, with adjacent quads, half a sector per store,
+// 53.3; 8192 tokens of 48 heads from binary32 to bf16 the other way round, 55.2
+// against 51.2).
 #include "hq_paged.h"
 
 namespace hq {
@@ -23,28 +28,50 @@ namespace {
 
 constexpr int kPosThreads = 256;
 
-struct Unit {
-    float v[8];
-};
-
-__device__ __forceinline__ Unit load_unit(const Rows &r, int64_t off)
+__device__ __forceinline__ void unpack(uint32_t w, float &lo, float &hi)
 {
-    Unit u;
-    if (r.f32) {
-        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(r.p) + off);
-        const float4 a = p[0], b = p[1];
-        u.v[0] = a.x; u.v[1] = a.y; u.v[2] = a.z; u.v[3] = a.w;
-        u.v[4] = b.x; u.v[5] = b.y; u.v[6] = b.z; u.v[7] = b.w;
-    } else {
-        const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(r.p) + off);
-        const uint32_t ww[4] = { w.x, w.y, w.z, w.w };
+    lo = __uint_as_float(w << 16);
+    hi = __uint_as_float(w & 0xffff0000u);
+}
+
+// The quads of item j of a span of n elements that begins at `base`
+template <bool QUADS>
+__device__ __forceinline__ void places(int base, int n, int j, int (&at)[4])
+{
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            u.v[2 * i] = __uint_as_float(ww[i] << 16);
-            u.v[2 * i + 1] = __uint_as_float(ww[i] & 0xffff0000u);
+    for (int q = 0; q < 4; q++) at[q] = base + (QUADS ? q * (n / 4) + 4 * j : (q >> 1) * (n / 2) + 8 * j + 4 * (q & 1));
+}
+
+template <bool QUADS>
+__device__ __forceinline__ void load16(const Rows &r, int64_t off, const int (&at)[4], float (&v)[16])
+{
+    const uint16_t *b = static_cast<const uint16_t *>(r.p) + off;
+    if (r.f32) {
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            const float4 x = *reinterpret_cast<const float4 *>(static_cast<const float *>(r.p) + off + at[q]);
+            v[4 * q] = x.x;
+            v[4 * q + 1] = x.y;
+            v[4 * q + 2] = x.z;
+            v[4 * q + 3] = x.w;
+        }
+    } else if constexpr (QUADS) {
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(b + at[q]);
+            unpack(x.x, v[4 * q], v[4 * q + 1]);
+            unpack(x.y, v[4 * q + 2], v[4 * q + 3]);
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < 4; q += 2) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(b + at[q]);
+            unpack(x.x, v[4 * q], v[4 * q + 1]);
+            unpack(x.y, v[4 * q + 2], v[4 * q + 3]);
+            unpack(x.z, v[4 * q + 4], v[4 * q + 5]);
+            unpack(x.w, v[4 * q + 6], v[4 * q + 7]);
         }
     }
-    return u;
 }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi)
@@ -53,15 +80,24 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&p);
 }
 
-__device__ __forceinline__ void store_unit(void *p, int f32, int64_t off, const Unit &u)
+template <bool QUADS>
+__device__ __forceinline__ void store16(void *p, int f32, int64_t off, const int (&at)[4], const float (&v)[16])
 {
+    uint16_t *b = static_cast<uint16_t *>(p) + off;
     if (f32) {
-        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p) + off);
-        o[0] = make_float4(u.v[0], u.v[1], u.v[2], u.v[3]);
-        o[1] = make_float4(u.v[4], u.v[5], u.v[6], u.v[7]);
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+            *reinterpret_cast<float4 *>(static_cast<float *>(p) + off + at[q]) =
+                make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+    } else if constexpr (QUADS) {
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+            *reinterpret_cast<uint2 *>(b + at[q]) = make_uint2(pack2(v[4 * q], v[4 * q + 1]), pack2(v[4 * q + 2], v[4 * q + 3]));
     } else {
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + off) =
-            make_uint4(pack2(u.v[0], u.v[1]), pack2(u.v[2], u.v[3]), pack2(u.v[4], u.v[5]), pack2(u.v[6], u.v[7]));
+#pragma unroll
+        for (int q = 0; q < 4; q += 2)
+            *reinterpret_cast<uint4 *>(b + at[q]) = make_uint4(pack2(v[4 * q], v[4 * q + 1]), pack2(v[4 * q + 2], v[4 * q + 3]),
+                                                               pack2(v[4 * q + 4], v[4 * q + 5]), pack2(v[4 * q + 6], v[4 * q + 7]));
     }
 }
 
@@ -82,7 +118,10 @@ __device__ __forceinline__ float2 cos_sin(uint64_t phase)
 }  // namespace
 
 // Item i of a token: 16 elements of head i / (head_dim / 16) (q heads, then k,
-// then v).  Shared table: pair 8 j + 2 c + e of a token at float4 c * units + j.
+// then v).  The shared table holds each item's 8 pairs in the order of its
+// elements, two to a float4: float4 c of item j at c * items of the head + j.
+// An item's pairs are `groups` runs of 8 / groups consecutive ones.
+template <bool QUADS>
 __global__ void __launch_bounds__(kPosThreads) positions_kernel(const PosArgs a)
 {
     extern __shared__ float4 sm_cs[];
@@ -91,6 +130,7 @@ __global__ void __launch_bounds__(kPosThreads) positions_kernel(const PosArgs a)
     const int items = (a.heads + 2 * a.kvh) * units;
     const int64_t tok0 = (int64_t)blockIdx.x * a.tokens_per_block;
     const int nt = (int)min((int64_t)a.tokens_per_block, a.tokens - tok0);
+    const int gshift = (QUADS ? 1 : 0) + (a.interleaved ? 1 : 0);  // log2 of the groups
 
     for (int e = tid; e < nt * pairs; e += kPosThreads) {
         const int t = e / pairs, i = e - t * pairs;
@@ -98,7 +138,8 @@ __global__ void __launch_bounds__(kPosThreads) positions_kernel(const PosArgs a)
         float2 cs = cos_sin(phase);
         cs.x *= a.amplitude;
         cs.y *= a.inverse ? -a.amplitude : a.amplitude;
-        const int j = i >> 3, c = (i >> 1) & 3;
+        const int run = pairs >> gshift, g = i / run, k = i - g * run;  // pair k of group g
+        const int j = k >> (3 - gshift), c = (g << (2 - gshift)) + ((k >> 1) & ((4 >> gshift) - 1));
         reinterpret_cast<float2 *>(sm_cs + (t * 4 + c) * runits + j)[i & 1] = cs;
     }
     __syncthreads();
@@ -110,8 +151,11 @@ __global__ void __launch_bounds__(kPosThreads) positions_kernel(const PosArgs a)
         const int j = w - head * units;
         const int64_t tok = tok0 + t;
         const bool rotated = j < runits && head < a.heads + a.kvh;
-        const int half = rotated && !a.interleaved;
-        const int e0 = half ? 8 * j : 16 * j, e1 = half ? a.rotary / 2 + 8 * j : 16 * j + 8;
+        int at[4];
+        // the rotated span of a head, the rest of it, or all of a value's
+        if (head >= a.heads + a.kvh) places<QUADS>(0, a.head_dim, j, at);
+        else if (rotated) places<QUADS>(0, a.rotary, j, at);
+        else places<QUADS>(a.rotary, a.head_dim - a.rotary, j - runits, at);
         int64_t slot = 0;
         if (a.slots) {
             slot = a.slots[tok];
@@ -142,7 +186,8 @@ __global__ void __launch_bounds__(kPosThreads) positions_kernel(const PosArgs a)
             to = (slot >> a.page_shift) * a.page_stride + head * a.head_stride +
                  (slot & ((1 << a.page_shift) - 1)) * a.slot_stride;
         }
-        Unit u0 = load_unit(src, from + e0), u1 = load_unit(src, from + e1);
+        float v[16];
+        load16<QUADS>(src, from, at, v);
         if (rotated) {
             float cs[16];
 #pragma unroll
@@ -153,26 +198,20 @@ __global__ void __launch_bounds__(kPosThreads) positions_kernel(const PosArgs a)
                 cs[4 * c + 2] = f.z;
                 cs[4 * c + 3] = f.w;
             }
-            if (half) {
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    const float x1 = u0.v[i], x2 = u1.v[i], co = cs[2 * i], si = cs[2 * i + 1];
-                    u0.v[i] = x1 * co - x2 * si;
-                    u1.v[i] = x2 * co + x1 * si;
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    Unit &u = i < 4 ? u0 : u1;
-                    const int k = 2 * (i & 3);
-                    const float x1 = u.v[k], x2 = u.v[k + 1], co = cs[2 * i], si = cs[2 * i + 1];
-                    u.v[k] = x1 * co - x2 * si;
-                    u.v[k + 1] = x2 * co + x1 * si;
+            for (int i = 0; i < 8; i++) {
+                if (a.interleaved) {
+                    const float x1 = v[2 * i], x2 = v[2 * i + 1], co = cs[2 * i], si = cs[2 * i + 1];
+                    v[2 * i] = x1 * co - x2 * si;
+                    v[2 * i + 1] = x2 * co + x1 * si;
+                } else {
+                    const float x1 = v[i], x2 = v[8 + i], co = cs[2 * i], si = cs[2 * i + 1];
+                    v[i] = x1 * co - x2 * si;
+                    v[8 + i] = x2 * co + x1 * si;
                 }
             }
         }
-        store_unit(dst, f32, to + e0, u0);
-        store_unit(dst, f32, to + e1, u1);
+        store16<QUADS>(dst, f32, to, at, v);
     }
 }
 
@@ -187,7 +226,8 @@ cudaError_t launch_positions(const PosArgs &args, cudaStream_t s)
     a.tokens_per_block = a.tokens >= 16 * (int64_t)sm_count() ? 4 : 1;
     const int64_t blocks = (a.tokens + a.tokens_per_block - 1) / a.tokens_per_block;
     const size_t smem = (size_t)a.tokens_per_block * a.rotary / 2 * sizeof(float2);
-    positions_kernel<<<(unsigned)blocks, kPosThreads, smem, s>>>(a);
+    const bool quads = a.kvh == 0 && a.y.f32;
+    (quads ? positions_kernel<true> : positions_kernel<false>)<<<(unsigned)blocks, kPosThreads, smem, s>>>(a);
     return cudaGetLastError();
 }
 
