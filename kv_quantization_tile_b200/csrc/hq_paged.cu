@@ -539,46 +539,50 @@ paged_few_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, co
 namespace {
 
 // 8 elements as they lie: 32 bytes of binary32, 16 of bf16
+template <bool F32>
 struct Raw8 {
-    uint4 a, b;
+    uint32_t w[F32 ? 8 : 4];
 };
 
-__device__ __forceinline__ Raw8 load_raw(const Rows &r, int64_t tok, int64_t h, int u)
+// The thread's two quads of a row of d elements: adjacent (16-byte accesses of
+// bf16), or half a row apart (QUADS), which keeps a warp's binary32 stores
+// contiguous.
+template <bool F32, bool QUADS>
+__device__ __forceinline__ Raw8<F32> load_raw(const Rows &r, int64_t tok, int64_t h, int u, int d)
 {
-    const int64_t off = tok * r.ts + h * r.hs + 8 * u;
-    Raw8 x;
-    if (r.f32) {
-        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(r.p) + off);
-        x.a = p[0];
-        x.b = p[1];
+    const int64_t off = tok * r.ts + h * r.hs + (QUADS ? 4 : 8) * u;
+    Raw8<F32> x;
+    if constexpr (F32) {
+        const float *p = static_cast<const float *>(r.p) + off;
+        const uint4 a = *reinterpret_cast<const uint4 *>(p), b = *reinterpret_cast<const uint4 *>(p + (QUADS ? d / 2 : 4));
+        x.w[0] = a.x, x.w[1] = a.y, x.w[2] = a.z, x.w[3] = a.w;
+        x.w[4] = b.x, x.w[5] = b.y, x.w[6] = b.z, x.w[7] = b.w;
+    } else if constexpr (QUADS) {
+        const uint16_t *p = static_cast<const uint16_t *>(r.p) + off;
+        const uint2 a = *reinterpret_cast<const uint2 *>(p), b = *reinterpret_cast<const uint2 *>(p + d / 2);
+        x.w[0] = a.x, x.w[1] = a.y, x.w[2] = b.x, x.w[3] = b.y;
     } else {
-        x.a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(r.p) + off);
+        const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(r.p) + off);
+        x.w[0] = a.x, x.w[1] = a.y, x.w[2] = a.z, x.w[3] = a.w;
     }
     return x;
 }
 
-__device__ __forceinline__ void as_float(const Rows &r, const Raw8 &x, float (&v)[8])
+template <bool F32>
+__device__ __forceinline__ float element(const Raw8<F32> &x, int i)
 {
-    const uint32_t a[4] = { x.a.x, x.a.y, x.a.z, x.a.w }, b[4] = { x.b.x, x.b.y, x.b.z, x.b.w };
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        if (r.f32) {
-            v[i] = __uint_as_float(a[i]);
-            v[4 + i] = __uint_as_float(b[i]);
-        } else {
-            v[2 * i] = __uint_as_float(a[i] << 16);
-            v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
-        }
-    }
+    if constexpr (F32) return __uint_as_float(x.w[i]);
+    else return __uint_as_float(i & 1 ? x.w[i / 2] & 0xffff0000u : x.w[i / 2] << 16);
 }
 
-__device__ __forceinline__ void store8(const Rows &r, int64_t tok, int64_t h, int u, const float (&v)[8])
+template <bool F32>
+__device__ __forceinline__ void store8(const Rows &r, int64_t tok, int64_t h, int u, int d, const float (&v)[8])
 {
-    const int64_t off = tok * r.ts + h * r.hs + 8 * u;
-    if (r.f32) {
-        float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(r.p) + off);
-        p[0] = make_float4(v[0], v[1], v[2], v[3]);
-        p[1] = make_float4(v[4], v[5], v[6], v[7]);
+    const int64_t off = tok * r.ts + h * r.hs + (F32 ? 4 : 8) * u;
+    if constexpr (F32) {
+        float *p = static_cast<float *>(r.p) + off;
+        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4 *>(p + d / 2) = make_float4(v[4], v[5], v[6], v[7]);
     } else {
         *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(r.p) + off) =
             make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
@@ -590,10 +594,13 @@ __device__ __forceinline__ void store8(const Rows &r, int64_t tok, int64_t h, in
 // out = (wa a + wb b) / (wa + wb), w = exp(lse - max).  A part that saw nothing
 // (lse -inf) has weight 0 and what its row holds is not used.  HBM-bound: three
 // rows per (token, head).  A thread takes the same 8 elements of kMergeRows rows
-// at once, all loads ahead of the first use (one row at a time, its loads after
-// its lse: 37 us for 4099 x 32 x 128, two bf16 parts and a binary32 result).
-constexpr int kMergeRows = 4;
+// at once, all loads ahead of the first use (4099 x 32 x 128, two bf16 parts and
+// a binary32 result: 25.7 us; four rows 29.3; one row, its loads after its lse,
+// 37).
+constexpr int kMergeRows = 2;
 
+// A32, B32, O32: binary32 parts and output
+template <bool A32, bool B32, bool O32>
 __global__ void __launch_bounds__(256) merge_kernel(const MergeArgs a)
 {
     const int units = a.head_dim / 8, per = 256 / units;  // units of a row, rows of a block's pass
@@ -602,7 +609,8 @@ __global__ void __launch_bounds__(256) merge_kernel(const MergeArgs a)
     const int64_t rows = a.tokens * a.heads;
     for (int64_t r0 = (int64_t)blockIdx.x * per * kMergeRows + lr; r0 < rows; r0 += (int64_t)gridDim.x * per * kMergeRows) {
         float la[kMergeRows], lb[kMergeRows];
-        Raw8 x[kMergeRows], y[kMergeRows];
+        Raw8<A32> x[kMergeRows];
+        Raw8<B32> y[kMergeRows];
         uint32_t tok[kMergeRows], h[kMergeRows];
 #pragma unroll
         for (int i = 0; i < kMergeRows; i++) {
@@ -612,8 +620,8 @@ __global__ void __launch_bounds__(256) merge_kernel(const MergeArgs a)
             h[i] = (uint32_t)row - tok[i] * (uint32_t)a.heads;
             la[i] = a.lse_a[row];
             lb[i] = a.lse_b[row];
-            x[i] = load_raw(a.a, tok[i], h[i], u);
-            y[i] = load_raw(a.b, tok[i], h[i], u);
+            x[i] = load_raw<A32, O32>(a.a, tok[i], h[i], u, a.head_dim);
+            y[i] = load_raw<B32, O32>(a.b, tok[i], h[i], u, a.head_dim);
         }
 #pragma unroll
         for (int i = 0; i < kMergeRows; i++) {
@@ -623,13 +631,11 @@ __global__ void __launch_bounds__(256) merge_kernel(const MergeArgs a)
             const float ea = la[i] == -INFINITY ? 0.0f : expf(la[i] - top), eb = lb[i] == -INFINITY ? 0.0f : expf(lb[i] - top);
             const float sum = ea + eb;
             const float wa = ea == 0.0f ? 0.0f : ea / sum, wb = eb == 0.0f ? 0.0f : eb / sum;
-            float v[8], z[8];
-            as_float(a.a, x[i], v);
-            as_float(a.b, y[i], z);
+            float v[8];
 #pragma unroll
             for (int k = 0; k < 8; k++)
-                v[k] = wa * (la[i] == -INFINITY ? 0.0f : v[k]) + wb * (lb[i] == -INFINITY ? 0.0f : z[k]);
-            store8(a.out, tok[i], h[i], u, v);
+                v[k] = wa * (la[i] == -INFINITY ? 0.0f : element(x[i], k)) + wb * (lb[i] == -INFINITY ? 0.0f : element(y[i], k));
+            store8<O32>(a.out, tok[i], h[i], u, a.head_dim, v);
             if (u == 0 && a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : top + logf(sum);
         }
     }
@@ -794,8 +800,13 @@ cudaError_t launch_merge(const MergeArgs &args, cudaStream_t s)
     MergeArgs a = args;
     a.heads_div = make_fastdiv((uint32_t)a.heads);
     const int64_t per = 256 / (a.head_dim / 8) * kMergeRows, rows = a.tokens * a.heads;
-    const int64_t blocks = (rows + per - 1) / per, most = (int64_t)sm_count() * 16;
-    merge_kernel<<<(unsigned)(blocks < most ? blocks : most), 256, 0, s>>>(a);
+    const int64_t blocks = (rows + per - 1) / per, most = (int64_t)sm_count() * 8;
+    using Kernel = void (*)(const MergeArgs);
+    const Kernel kernels[8] = { merge_kernel<false, false, false>, merge_kernel<false, false, true>,
+                                merge_kernel<false, true, false>,  merge_kernel<false, true, true>,
+                                merge_kernel<true, false, false>,  merge_kernel<true, false, true>,
+                                merge_kernel<true, true, false>,   merge_kernel<true, true, true> };
+    kernels[4 * a.a.f32 + 2 * a.b.f32 + a.out.f32]<<<(unsigned)(blocks < most ? blocks : most), 256, 0, s>>>(a);
     return cudaGetLastError();
 }
 
