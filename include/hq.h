@@ -463,7 +463,8 @@ int hq_rope(const hq_rows *x, const hq_rows *y, int64_t tokens, int heads, int h
 /* Append new tokens to the paged cache: k (rotated as by hq_rope) and v go to
  * slot slots[t] = page * page_size + offset of every KV head, rounded once to
  * bf16; q, if given, is rotated into q_out in the same launch.
- *   q, q_out   [tokens][q_heads][head_dim]; both NULL with q_heads = 0
+ *   q, q_out   [tokens][q_heads][head_dim]; both NULL with q_heads = 0; q_out
+ *              may be q itself (same strides and type)
  *   k, v       [tokens][pages->heads][pages->head_dim]
  *   turns      NULL with rotary_dim = 0: nothing is rotated (positions unused)
  *   slots      device int64 [tokens].  A negative slot skips the token (its
@@ -475,9 +476,10 @@ int hq_kv_append(const hq_rows *q, const hq_rows *q_out, int q_heads, const hq_r
                  int layout, float amplitude, const int64_t *slots, const hq_pages *pages, void *stream,
                  int32_t *d_status);
 
-/* Bytes of device workspace hq_paged_attention needs for these bounds (tile
- * counts, block shares, counters and partial results).  Depends on the SM
- * count of the current device.  Host only. */
+/* Bytes of device workspace hq_paged_attention needs for these bounds (work
+ * counts, block shares, counters and partial results; next to nothing where the
+ * call is one launch of thread-block clusters).  Calls with smaller bounds fit
+ * too.  Depends on the SM count of the current device.  Host only. */
 int hq_paged_attention_workspace_bytes(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_kv,
                                        int heads, int head_dim, int group, uint64_t *out);
 

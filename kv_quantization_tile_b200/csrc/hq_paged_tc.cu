@@ -641,7 +641,7 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                 const uint32_t page = (uint32_t)a.table[(int64_t)w.b * a.table_stride + (tok >> a.page_shift)];
                 if (page >= a.pages) {
                     if (a.status) atomicOr(a.status, kStatusIndex);
-                    return a.pages;
+                    return max(a.pages, 1u);
                 }
                 return page;
             };

@@ -189,6 +189,16 @@ def test_workspace_sizes():
             hq.hq_paged_attention_workspace_bytes(*bad)
 
 
+def test_a_workspace_for_larger_bounds_serves_smaller_calls():
+    rng = np.random.default_rng(0)
+    for _ in range(3000):
+        d, heads, group = int(rng.choice([64, 128, 256])), int(rng.integers(1, 33)), int(rng.integers(1, 9))
+        big = [int(2 ** rng.uniform(0, 8)), 0, int(2 ** rng.uniform(0, 9)), int(2 ** rng.uniform(0, 16))]
+        small = [max(1, int(v * rng.uniform(0, 1))) for v in big]
+        size = lambda b: hq.hq_paged_attention_workspace_bytes(b[0], b[0] * b[2], b[2], b[3], heads, d, group)  # noqa: E731
+        assert size(small) <= size(big), (small, big, d, heads, group)
+
+
 def test_cpu_tensors_and_wrong_shapes_are_refused():
     """The binding refuses what it could only turn into a bad device access."""
     x = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
