@@ -13,7 +13,7 @@
 // attention: a block serves up to GB query heads that share one KV head, so
 // each K and V tile is parsed once for all of them.
 //
-// Tokens are split across blocks (flash-decoding): a block writes, per query,
+// Tokens are split across blocks: a block writes, per query,
 // its maximum score m, its sum of exp(s - m) and its unnormalised rotated
 // output to the workspace; the last block of a (KV head, query chunk) to
 // finish -- found with a counter, no waiting -- merges the splits.

@@ -308,6 +308,33 @@ def test_attention_long_sequence_over_many_blocks():
     run_attention([129], [5003], 1, 4, 128, 32, seed=8)
 
 
+@pytest.mark.parametrize("d,longest", [(64, 17001), (128, 9001), (256, 4500)])
+@pytest.mark.parametrize("q,group", [(1, 3), (2, 16), (6, 8)])
+def test_attention_shares_that_cut_jobs(d, longest, q, group):
+    """Too many jobs for clusters and one long sequence: blocks take equal shares
+    of the tiles, and jobs cut between blocks are joined (16, 32 and 64 rows)."""
+    run_attention([q] * 20, [longest] + [50 + 37 * i for i in range(19)], 2, group, d, 64, seed=d + q)
+
+
+@pytest.mark.parametrize("d,kv", [(64, 17001), (128, 9001), (256, 4500)])
+def test_attention_shares_repeat_bit_for_bit(d, kv):
+    n = 20
+    kv_lens = [kv] + [70] * (n - 1)
+    kp, vp, table, _, _ = make_cache(kv_lens, 2, d, 128, 2)
+    q = randn(n, 8, d, seed=1).to(DEV)
+    pool = hq.Pages(kp.to(DEV), vp.to(DEV))
+    ws = hq.alloc_paged_attention_workspace(n, n, 1, kv, 2, 4, d)
+    got = []
+    for fill in (0, 255, None, None):
+        if fill is not None:
+            ws.fill_(fill)
+        out, lse = torch.empty_like(q), torch.empty(n, 8, device=DEV)
+        hq.hq_paged_attention(q, starts([1] * n).to(DEV), i32(*kv_lens), pool, table.to(DEV), 0.09, out, ws, max_q=1,
+                              max_kv=kv, lse=lse)
+        got.append((out, lse))
+    assert all(torch.equal(o, got[0][0]) and torch.equal(s, got[0][1]) for o, s in got)
+
+
 def test_attention_many_sequences():
     """More sequences than one pass of the plan counts, lengths 0 to 40."""
     n = 1500
