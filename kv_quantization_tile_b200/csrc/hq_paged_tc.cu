@@ -5,6 +5,8 @@
 // with row tiles of 256 packed rows (two MMA tiles of 128; one of 128 at
 // head_dim 256, whose output fills the tensor memory) and token tiles of 128
 // (64).  One block per SM, its warps in roles:
+//   * the job warp walks the block's share and describes each segment (a job or
+//     a part of one) to the others, through a ring in shared memory;
 //   * the load warp copies K and V tiles page by page with TMA (128-byte
 //     swizzle, one copy per page and 64 columns) into a ring of buffers;
 //   * the product warp issues S = Q K^T (both operands in shared memory) and
@@ -34,7 +36,6 @@ namespace hq {
 
 namespace {
 
-constexpr int kPoly = 1;       // of 8 pairs of weights, those computed on the fma pipe
 constexpr float kGrow = 24.0f;  // powers of two by which a tile may exceed the running maximum
 
 template <int D>
@@ -42,7 +43,7 @@ struct Many {
     static constexpr int NT = D == 256 ? 1 : 2;        // MMA tiles of 128 rows
     static constexpr int RT = 128 * NT;
     static constexpr int T = D == 256 ? 64 : 128;      // tokens per tile
-    static constexpr int THREADS = 256 * NT + 64;
+    static constexpr int THREADS = 256 * NT + 96;
     static constexpr uint32_t TILE = T * D * 2;        // one K or V tile
     static constexpr uint32_t QTILE = 128 * D * 2;
     static constexpr int STAGES = D == 64 ? 8 : 5;
@@ -50,6 +51,19 @@ struct Many {
     // tensor memory: O of each MMA tile, then two score buffers
     static constexpr uint32_t O_COL = 0, S_COL = 256;
 };
+
+// A segment of the block's share, as the job warp describes it.
+struct Segment {
+    int valid;            // 0: the share has ended
+    int b, h, q0, rows;   // sequence, KV head, first query row, rows of the sequence
+    int r0;               // first packed row of the row tile
+    int nq, kv;           // new and cached tokens
+    int tile, count;      // first tile (of T tokens), tiles
+    int lo, hi;           // cached tokens that any row of the job sees
+    int whole;            // the job is not cut
+    int slot, c0, c1;     // if it is: this part's slot, the blocks of the first and the last part
+};
+constexpr int kSegments = 4;
 
 // Shared-memory descriptor of a 128-byte-swizzled operand: 8-row groups of 128
 // bytes `sbo` apart; `lbo` is the distance between blocks of 64 elements along
@@ -128,37 +142,15 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return d;
 }
 
-// 2^x of a pair on the fma pipe, for x <= kGrow and a little over: x = n + f, n
-// its nearest integer (read from the low bits of x + 1.5 2^23), 2^f by a
-// minimax polynomial of degree 5 on [-1/2, 1/2] (relative error 7.5e-8, 2.2e-7
-// in binary32, as ex2.approx's 2^-22), n added to the exponent.  Below 2^-125
-// the result is held there; a NaN stays one.
-__device__ __forceinline__ float2 ex2_poly(float2 x)
-{
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.x) : "f"(-125.0f));
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.y) : "f"(-125.0f));
-    const float2 magic = splat2(12582912.0f);
-    const float2 t = add2(x, magic), f = sub2(x, sub2(t, magic));
-    float2 p = fma2(f, splat2(1.3276472454890609e-3f), splat2(9.675540961325169e-3f));
-    p = fma2(p, f, splat2(5.550713092088699e-2f));
-    p = fma2(p, f, splat2(0.24022120237350464f));
-    p = fma2(p, f, splat2(0.6931469440460205f));
-    p = fma2(p, f, splat2(1.0000001192092896f));
-    return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
-                       __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
-}
-
 // Weights of 32 columns of scores: 2^(s scale - off), packed to bf16 pairs,
-// their binary32 sum added to `sum`.  POLY of every 8 pairs go to the fma pipe,
-// the rest to the exponential unit.
-template <int POLY>
+// their binary32 sum added to `sum`.
 __device__ __forceinline__ void weights32(const uint32_t (&s)[32], float scale, float off, float2 (&sum)[2], uint32_t (&p)[16])
 {
     const float2 sc = splat2(scale), no = splat2(-off);
 #pragma unroll
     for (int i = 0; i < 16; i++) {
         const float2 x = fma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sc, no);
-        const float2 y = (i & 7) < POLY ? ex2_poly(x) : make_float2(ex2(x.x), ex2(x.y));
+        const float2 y = make_float2(ex2(x.x), ex2(x.y));
         sum[i & 1] = add2(sum[i & 1], y);
         p[i] = pack2(y.x, y.y);
     }
@@ -192,7 +184,8 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
     using C = Many<D>;
     constexpr int NT = C::NT, RT = C::RT, T = C::T, STAGES = C::STAGES;
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t s_bar[2 * STAGES + NT * 2 + 6 + 1];
+    __shared__ __align__(8) uint64_t s_bar[2 * STAGES + NT * 2 + 6 + 1 + 2 * kSegments];
+    __shared__ Segment s_seg[kSegments];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_fail;
     __shared__ int s_last[NT];
@@ -209,6 +202,8 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
     auto p_full = [&](int b) { return bar0 + 8u * (uint32_t)(2 * STAGES + 2 * NT + 2 + b); };
     auto p_half = [&](int b) { return bar0 + 8u * (uint32_t)(2 * STAGES + 2 * NT + 4 + b); };  // the first 32 weights of either half
     const uint32_t fix_bar = bar0 + 8u * (uint32_t)(2 * STAGES + 2 * NT + 6);
+    auto seg_full = [&](uint32_t k) { return fix_bar + 8u * (1 + k); };
+    auto seg_empty = [&](uint32_t k) { return fix_bar + 8u * (1 + kSegments + k); };
 
     if (warp == 0) tmem_alloc(smem_u32(&s_tmem), 512);
     if (tid == 0) {
@@ -227,6 +222,10 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
             mbar_init(p_half(b), 8);
         }
         mbar_init(fix_bar, 1);
+        for (int k = 0; k < kSegments; k++) {
+            mbar_init(seg_full(k), 1);
+            mbar_init(seg_empty(k), 8 * NT + 2);  // the softmax warps, products, loads
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     tc_fence_before();
@@ -245,8 +244,14 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
         prefetch_map(&vmap);
     }
     pdl_wait();
-    SegWalk<T, RT> w;
-    const bool work = w.begin(a);
+    // segment i (whether there is one), and this warp's leave of it
+    auto segment = [&](uint32_t i) -> bool {
+        return __all_sync(FULL, wait(seg_full(i % kSegments), (i / kSegments) & 1u)) && s_seg[i % kSegments].valid;
+    };
+    auto leave = [&](uint32_t i) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(seg_empty(i % kSegments));
+    };
 
     if (wg < 2 * NT) {
         // ------------------------------------------------ softmax
@@ -258,14 +263,14 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
         // This warp's half of 32 query rows of a segment, copied on the side (zeros
         // past the last row), then handed over.
         constexpr int CH = D / 16;  // chunks per half row, copies per lane
-        auto copy_queries = [&](const SegWalk<T, RT> &x) {
+        auto copy_queries = [&](const Segment &x) {
 #pragma unroll 1
             for (int e = lane; e < 32 * CH; e += 32) {
-                const int rr = wl * 32 + e / CH, c = hf * CH + e % CH, r = x.rt * RT + t * 128 + rr;
-                const bool valid = r < x.s.rows && a.q_mode != 2;
+                const int rr = wl * 32 + e / CH, c = hf * CH + e % CH, r = x.r0 + t * 128 + rr;
+                const bool valid = r < x.rows && a.q_mode != 2;
                 const int j = (int)fast_div((uint32_t)r, a.group_div), gg = r - j * a.group;
                 const uint16_t *q = static_cast<const uint16_t *>(a.q.p);
-                if (valid) q += (x.s.q0 + j) * a.q.ts + (x.h * a.group + gg) * a.q.hs + 8 * c;
+                if (valid) q += (x.q0 + j) * a.q.ts + (x.h * a.group + gg) * a.q.hs + 8 * c;
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sq + t * C::QTILE + swizzled_off(128, rr, c)),
                              "l"(q), "r"(valid ? 16 : 0) : "memory");
             }
@@ -284,23 +289,24 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full(t));
         };
-        bool more = work;
+        uint32_t i = 0;
+        bool more = segment(0);
         if (more) {
-            copy_queries(w);
+            copy_queries(s_seg[0]);
             hand_queries();
         }
-        while (more) {
-            const int r = w.rt * RT + t * 128 + wl * 32 + lane, rows = w.s.rows, q0 = w.s.q0, h = w.h;
+        for (; more; i++) {
+            const Segment &x = s_seg[i % kSegments];
+            const int r = x.r0 + t * 128 + wl * 32 + lane, rows = x.rows, count = x.count;
             int rlo = 0, rhi = 0;
             if (r < rows) {
                 const int j = (int)fast_div((uint32_t)r, a.group_div);
-                seen_range(a, w.s, j, j, rlo, rhi);
+                const Seq s{ x.q0, x.nq, x.kv, rows };
+                seen_range(a, s, j, j, rlo, rhi);
             }
-            SegWalk<T, RT> after = w;
-            more = after.next(a);  // (its lengths are read while the first scores are computed)
             float m = -INFINITY, l = 0.0f;
             bool ok = true;
-            for (int tile = w.first; tile < w.first + w.count; tile++, g++) {
+            for (int n = 0; n < count; n++, g++) {
                 const int b = NT == 2 ? t : (int)(g & 1u);
                 const uint32_t par = NT == 2 ? g & 1u : (g >> 1) & 1u;
                 const uint32_t ts = tmem + lanes + C::S_COL + (uint32_t)(b * T);
@@ -309,14 +315,17 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                 // Every product with V is waited for in turn (a barrier's phase can
                 // only be told from the one before it).  With two MMA tiles S comes
                 // after that product anyway; with one, S runs ahead of it.
-                if (NT == 1 && tile > w.first) ok = wait(o_full(t), (g - 1u) & 1u) && ok;
+                if (NT == 1 && n > 0) ok = wait(o_full(t), (g - 1u) & 1u) && ok;
                 ok = __all_sync(FULL, ok);
                 tc_fence_after();
                 // the last scores are there, so the queries are free: the next
                 // segment's take their place
-                if (tile + 1 == w.first + w.count && more && ok) copy_queries(after);
+                if (n + 1 == count) {
+                    more = segment(i + 1);
+                    if (more && ok) copy_queries(s_seg[(i + 1) % kSegments]);
+                }
                 const uint32_t mine = ts + (uint32_t)(hf * (T / 2));  // this half's scores, then its weights
-                const int tok0 = (w.t0 + tile) * T + hf * (T / 2);
+                const int tok0 = (x.tile + n) * T + hf * (T / 2);
                 const bool edge = !__all_sync(FULL, rlo <= tok0 && rhi >= tok0 + T / 2);
                 auto mask = [&](int c, uint32_t (&s)[32]) {
                     const int from = rlo - tok0 - 32 * c, to_ = rhi - tok0 - 32 * c;
@@ -325,14 +334,12 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                         if (i < from || i >= to_) s[i] = 0xff800000u;
                 };
                 // Weights are rounded to bf16 for the product with V (2^-8 of
-                // each, independent); their sum keeps binary32.  Masked columns
-                // need exact zeros: edge tiles take no polynomial.
+                // each, independent); their sum keeps binary32.
                 float2 sum[2] = { make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f) };
                 uint32_t s[32], p[16];
                 auto weights = [&]() {
                     const float off = m == -INFINITY ? 0.0f : m;  // nothing seen yet: every weight is 0
-                    if (edge) weights32<0>(s, a.scale_log2, off, sum, p);
-                    else weights32<kPoly>(s, a.scale_log2, off, sum, p);
+                    weights32(s, a.scale_log2, off, sum, p);
                 };
                 auto hand_over = [&](int c, uint32_t bar) {  // over scores already read
                     tmem_st16(mine + (uint32_t)(16 * c), p);
@@ -367,7 +374,7 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                 // tile that raises it.
                 weights();
                 if (NC == 2) tmem_ld32(mine + 32, s);
-                if (named_any(pair, 64, tile == w.first || top > m + kGrow || !ok)) {
+                if (named_any(pair, 64, n == 0 || top > m + kGrow || !ok)) {
                     float *row = &s_row[t][wl * 32 + lane];
                     if (hf) *row = top;
                     if (named_any(pair, 64, !ok)) {  // a wait gave up: both warps leave
@@ -378,11 +385,11 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                     if (!hf) *row = top = fmaxf(top, *row);
                     named_sync(pair, 64);
                     top = *row;
-                    const bool grow = tile == w.first || top > m + kGrow;
-                    const float f = grow && tile > w.first ? ex2(m - top) : 1.0f;
+                    const bool grow = n == 0 || top > m + kGrow;
+                    const float f = grow && n > 0 ? ex2(m - top) : 1.0f;
                     if (grow) m = top;
                     l *= f;
-                    if (tile > w.first) {  // rescale O: the product before this one is complete
+                    if (n > 0) {  // rescale O: the product before this one is complete
                         ok = wait(o_full(t), (g - 1u) & 1u);  // (a failure is met at the next vote)
                         ok = __all_sync(FULL, ok);
                         tc_fence_after();
@@ -422,8 +429,7 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
             ok = ok && wait(o_full(t), (g - 1u) & 1u);
             if (named_any(9 + t, 256, !ok)) break;
             tc_fence_after();
-            const bool whole = w.whole();
-            const int slot = w.slot(), c0 = w.owner(a), c1 = w.last(a);
+            const bool whole = x.whole;
             if (more) hand_queries();  // its first scores come while O is written out
             const int rr = wl * 32 + lane;  // row of this MMA tile
             if (hf) s_row[t][rr] = l;
@@ -432,7 +438,7 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
             named_sync(pair, 64);
             l = s_row[t][rr];
             // partial results by MMA tile: m and l of its rows, then [D / 4][128] float4
-            float *part = a.part + ((int64_t)slot * NT + t) * (128 * (D + 2));
+            float *part = a.part + ((int64_t)x.slot * NT + t) * (128 * (D + 2));
             if (!whole && hf == 0) {
                 part[rr] = m;
                 part[128 + rr] = l;
@@ -442,8 +448,8 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
             int head = 0;
             if (r < rows) {
                 const int j = (int)fast_div((uint32_t)r, a.group_div);
-                tok = q0 + j;
-                head = h * a.group + r - j * a.group;
+                tok = x.q0 + j;
+                head = x.h * a.group + r - j * a.group;
             }
             const int64_t at = tok * a.out.ts + head * a.out.hs + hf * (D / 2);
             auto put = [&](int c, const float (&v)[32], float f, bool zero) {  // 32 of this half's columns of the row
@@ -486,6 +492,7 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
             bool write = whole;
             if (!whole) {
                 __threadfence();
+                const int c0 = x.c0, c1 = x.c1;
                 named_sync(9 + t, 256);
                 if (hf == 0 && rr == 0) s_last[t] = atomicAdd(a.counter + c0 * NT + t, 1u) == (unsigned)(c1 - c0);
                 named_sync(9 + t, 256);
@@ -495,42 +502,52 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                     auto part_at = [&](int k) {
                         return a.part + ((int64_t)(2 * k + (k == c0 ? 1 : 0)) * NT + t) * (128 * (D + 2));
                     };
+                    // the parts' factors, those of the first four kept
+                    float f4[4];
                     mt = -INFINITY;
-#pragma unroll 4
-                    for (int k = c0; k <= c1; k++) mt = fmaxf(mt, __ldcg(part_at(k) + rr));
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        f4[k] = c0 + k <= c1 ? __ldcg(part_at(c0 + k) + rr) : -INFINITY;
+                        mt = fmaxf(mt, f4[k]);
+                    }
+                    for (int k = c0 + 4; k <= c1; k++) mt = fmaxf(mt, __ldcg(part_at(k) + rr));
                     const float from = mt == -INFINITY ? 0.0f : mt;
                     lt = 0.0f;
-#pragma unroll 4
-                    for (int k = c0; k <= c1; k++) lt = fmaf(ex2(__ldcg(part_at(k) + rr) - from), __ldcg(part_at(k) + 128 + rr), lt);
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        f4[k] = ex2(f4[k] - from);
+                        if (c0 + k <= c1) lt = fmaf(f4[k], __ldcg(part_at(c0 + k) + 128 + rr), lt);
+                    }
+                    for (int k = c0 + 4; k <= c1; k++) lt = fmaf(ex2(__ldcg(part_at(k) + rr) - from), __ldcg(part_at(k) + 128 + rr), lt);
                     const float f = lt == 0.0f ? 0.0f : 1.0f / lt;
 #pragma unroll 1
                     for (int c = 0; c < D / 64; c++) {
                         float v[32];
 #pragma unroll
                         for (int i = 0; i < 32; i++) v[i] = 0.0f;
-#pragma unroll 1
-                        for (int k = c0; k <= c1; k += 2) {  // two parts' loads in flight
-                            const bool two = k < c1;
-                            const float e0 = ex2(__ldcg(part_at(k) + rr) - from), e1 = two ? ex2(__ldcg(part_at(k + 1) + rr) - from) : 0.0f;
-                            const float4 *p0 = reinterpret_cast<const float4 *>(part_at(k) + 256) + (hf * (D / 8) + 8 * c) * 128 + rr;
-                            const float4 *p1 = reinterpret_cast<const float4 *>(part_at(k + 1) + 256) + (hf * (D / 8) + 8 * c) * 128 + rr;
+                        auto add = [&](int k, float e) {
+                            const float4 *p = reinterpret_cast<const float4 *>(part_at(k) + 256) + (hf * (D / 8) + 8 * c) * 128 + rr;
 #pragma unroll
                             for (int i = 0; i < 8; i++) {
-                                const float4 x = __ldcg(p0 + i * 128);
-                                const float4 y = two ? __ldcg(p1 + i * 128) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                                v[4 * i] = fmaf(e1, y.x, fmaf(e0, x.x, v[4 * i]));
-                                v[4 * i + 1] = fmaf(e1, y.y, fmaf(e0, x.y, v[4 * i + 1]));
-                                v[4 * i + 2] = fmaf(e1, y.z, fmaf(e0, x.z, v[4 * i + 2]));
-                                v[4 * i + 3] = fmaf(e1, y.w, fmaf(e0, x.w, v[4 * i + 3]));
+                                const float4 x = __ldcg(p + i * 128);
+                                v[4 * i] = fmaf(e, x.x, v[4 * i]);
+                                v[4 * i + 1] = fmaf(e, x.y, v[4 * i + 1]);
+                                v[4 * i + 2] = fmaf(e, x.z, v[4 * i + 2]);
+                                v[4 * i + 3] = fmaf(e, x.w, v[4 * i + 3]);
                             }
-                        }
+                        };
+#pragma unroll
+                        for (int k = 0; k < 4; k++)
+                            if (c0 + k <= c1) add(c0 + k, f4[k]);
+#pragma unroll 1
+                        for (int k = c0 + 4; k <= c1; k++) add(k, ex2(__ldcg(part_at(k) + rr) - from));
                         put(c, v, f, lt == 0.0f);
                     }
                 }
             }
             if (write && hf == 0 && a.lse && r < rows)
                 a.lse[tok * (a.heads * a.group) + head] = lt == 0.0f ? -INFINITY : fmaf(mt, 0.693147180559945309f, logf(lt));
-            w = after;
+            leave(i);
         }
     } else {
         if ((warp & 3) == 0) {
@@ -538,14 +555,14 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
             // The warp walks as one, so addresses stay in uniform registers;
             // one elected lane issues (always the same one: a commit covers
             // the products of its own thread).
-            if (work) {
+            if (segment(0)) {
                 constexpr uint32_t ID_S = make_idesc_bf16(128, T);
                 constexpr uint32_t ID_O = make_idesc_bf16(128, D) | (1u << 16);  // V is token-major: B not K-major
                 const bool one = elect_one();
                 const uint64_t qd = swizzled_desc(sq, 16, 1024), kd = swizzled_desc(ring, 16, 1024),
                                vd = swizzled_desc(ring, T * 128, 1024);
                 uint32_t slot = 0, phase = 0, g = 0, seg = 0;
-                bool ok = true, again = false;
+                bool ok = true;
                 auto take = [&]() -> uint32_t {  // the next tile of the ring, landed
                     ok = ok && wait(kv_full(slot), phase);
                     const uint32_t s = slot;
@@ -592,8 +609,8 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                     }
                     if (!ok) break;
                     commit(kv_empty(k0));
-                    const int count = w.count;
-                    again = w.next(a);  // (its lengths are read while the first softmax runs)
+                    const int count = s_seg[seg % kSegments].count;
+                    leave(seg);
                     for (int j = 0; j < count && ok; j++, g++) {
                         const bool more = j + 1 < count;
                         const uint32_t k = more ? take() : 0u;
@@ -625,9 +642,9 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                         if (NT == 2 && more) commit(kv_empty(k));
                     }
                     seg++;
-                } while (ok && again);
+                } while (ok && segment(seg));
             }
-        } else if ((warp & 3) == 1 && work) {
+        } else if ((warp & 3) == 1) {
             // -------------------------------------------- loads
             const int page_rows = 1 << a.page_shift, box = page_rows < T ? page_rows : T;
             const int col = lane % (D / 64), pg = lane / (D / 64);
@@ -635,38 +652,39 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
             bool ok = true;
             // this lane's page of a tile (past the pool, where TMA fills zeros,
             // for a number outside it); read a tile ahead of its use
-            auto page_of = [&](int tile) -> uint32_t {
-                const int tok = (w.t0 + tile) * T + pg * box;
-                if (tile >= w.first + w.count || pg * box >= T || tok >= w.hi || tok + box <= w.lo) return 0;
-                const uint32_t page = (uint32_t)a.table[(int64_t)w.b * a.table_stride + (tok >> a.page_shift)];
+            Segment x{};
+            auto page_of = [&](int n) -> uint32_t {
+                const int tok = (x.tile + n) * T + pg * box;
+                if (n >= x.count || pg * box >= T || tok >= x.hi || tok + box <= x.lo) return 0;
+                const uint32_t page = (uint32_t)a.table[(int64_t)x.b * a.table_stride + (tok >> a.page_shift)];
                 if (page >= a.pages) {
                     if (a.status) atomicOr(a.status, kStatusIndex);
                     return max(a.pages, 1u);
                 }
                 return page;
             };
-            auto load = [&](int tile, bool is_v, uint32_t page) {
+            auto load = [&](int n, bool is_v, uint32_t page) {
                 ok = ok && wait(kv_empty(slot), phase ^ 1u);
                 ok = __all_sync(FULL, ok);
                 if (!ok) return;
-                const int tok0 = (w.t0 + tile) * T, tok = tok0 + pg * box;
+                const int tok0 = (x.tile + n) * T, tok = tok0 + pg * box;
                 const uint32_t dst = ring + slot * C::TILE;
                 // rows of V outside the job's tokens meet weight 0: they must be finite
-                const bool fix = is_v && (tok0 < w.lo || tok0 + T > w.hi);
+                const bool fix = is_v && (tok0 < x.lo || tok0 + T > x.hi);
                 const uint32_t bar = fix ? fix_bar : kv_full((int)slot);
-                const bool mine = pg * box < T && tok < w.hi && tok + box > w.lo;
-                const uint32_t n = __popc(__ballot_sync(FULL, mine));
-                if (lane == 0) mbar_expect(bar, n * (uint32_t)box * 128u);
+                const bool mine = pg * box < T && tok < x.hi && tok + box > x.lo;
+                const uint32_t boxes = __popc(__ballot_sync(FULL, mine));
+                if (lane == 0) mbar_expect(bar, boxes * (uint32_t)box * 128u);
                 __syncwarp();
                 if (mine)
                     tma_page(dst + (uint32_t)(col * T * 128 + pg * box * 128), is_v ? &vmap : &kmap, bar, col * 64,
-                             tok & (page_rows - 1), w.h, (int)page);
+                             tok & (page_rows - 1), x.h, (int)page);
                 if (fix) {
                     ok = wait(fix_bar, fixes & 1u);
                     fixes++;
                     for (int e = lane; e < T * (D / 8); e += 32) {
                         const int r = e / (D / 8), c = e % (D / 8);
-                        if (tok0 + r < w.lo || tok0 + r >= w.hi)
+                        if (tok0 + r < x.lo || tok0 + r >= x.hi)
                             asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(dst + swizzled_off(T, r, c)), "r"(0u) : "memory");
                     }
                     fence_async_smem();
@@ -678,21 +696,57 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                     phase ^= 1u;
                 }
             };
-            do {
-                const int e = w.first + w.count;
-                uint32_t here = page_of(w.first), next = page_of(w.first + 1);
-                load(w.first, false, here);
-                for (int tile = w.first; tile < e && ok; tile++) {
-                    const uint32_t after = page_of(tile + 2);
-                    if (tile + 1 < e) load(tile + 1, false, next);
-                    load(tile, true, here);
+            for (uint32_t i = 0; ok && segment(i); i++) {
+                x = s_seg[i % kSegments];
+                leave(i);
+                uint32_t here = page_of(0), next = page_of(1);
+                load(0, false, here);
+                for (int n = 0; n < x.count && ok; n++) {
+                    const uint32_t after = page_of(n + 2);
+                    if (n + 1 < x.count) load(n + 1, false, next);
+                    load(n, true, here);
                     here = next;
                     next = after;
                 }
-            } while (ok && w.next(a));
+            }
             // after a wait that gave up, let the copies in flight land
             if (!ok)
                 for (int s = 0; s < STAGES; s++) mbar_wait(kv_full(s), s < (int)slot ? phase : phase ^ 1u);
+        } else {
+            // -------------------------------------------- jobs
+            SegWalk<T, RT> w;
+            bool go = w.begin(a);
+            for (uint32_t i = 0;; i++) {
+                if (!__all_sync(FULL, wait(seg_empty(i % kSegments), ((i / kSegments) & 1u) ^ 1u))) break;
+                if (lane == 0) {
+                    Segment x{};
+                    x.valid = go;
+                    if (go) {
+                        x.b = w.b;
+                        x.h = w.h;
+                        x.q0 = w.s.q0;
+                        x.rows = w.s.rows;
+                        x.r0 = w.rt * RT;
+                        x.nq = w.s.nq;
+                        x.kv = w.s.kv;
+                        x.tile = w.t0 + w.first;
+                        x.count = w.count;
+                        x.lo = w.lo;
+                        x.hi = w.hi;
+                        x.whole = w.whole();
+                        if (!x.whole) {
+                            x.slot = w.slot();
+                            x.c0 = w.owner(a);
+                            x.c1 = w.last(a);
+                        }
+                    }
+                    s_seg[i % kSegments] = x;
+                    mbar_arrive(seg_full(i % kSegments));
+                }
+                __syncwarp();
+                if (!go) break;
+                go = w.next(a);
+            }
         }
     }
     __syncthreads();
