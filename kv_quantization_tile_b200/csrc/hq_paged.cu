@@ -693,13 +693,19 @@ cudaError_t launch_plan_many(const PagedArgs &many, const PagedArgs &few, int he
 
 }  // namespace
 
-// Which kernel takes which sequences.  Up to 64 rows per sequence (new tokens x
-// group) the mma.sync kernel keeps pace with HBM: 16, 32 or 64 rows per tile,
-// the fewest that hold the longest sequence's rows.  Beyond, the tcgen05
-// kernel; in a batch, sequences of at most 16 rows (tokens being decoded
-// beside a prompt) still go to the other one.  Blocks: as many as are resident
-// at once (shared memory allows 3, 2 and 1 of the mma.sync kernel per SM at
-// head_dim 64, 128 and 256, one of the tcgen05 kernel).
+// Which kernel takes which sequences, by the rows (new tokens x group) of the
+// longest.  The mma.sync kernel: 16, 32 or 64 rows per tile, the fewest that hold
+// them, or two tiles of 64.  It takes all calls of up to 64 rows (32 at head_dim
+// 256), and of up to 128 where the cache a job reads is short: the tcgen05 kernel
+// has the dearer start, the cheaper tile.  Measured (us; 8 KV heads, 8 sequences,
+// mma.sync / tcgen05), head_dim 128, 64 rows: 22 / 45 at 1024 tokens, 190 / 201 at
+// 16384; 128 rows: 33 / 43, 79 / 80 at 4096, 339 / 199; head_dim 64, 128 rows: 21 /
+// 35, 55 / 66, 202 / 176; head_dim 256, 4 KV heads, 4 sequences, 32 rows: 25 / 37,
+// 108 / 95; 128 rows: 29 / 36, 59 / 53 at 4096.  In a batch for the tcgen05 kernel,
+// sequences of at most 16 rows (tokens being decoded beside a prompt) still go to
+// the other one.  Blocks: as many as are resident at once (shared memory allows 3,
+// 2 and 1 of the mma.sync kernel per SM at head_dim 64, 128 and 256, one of the
+// tcgen05 kernel).
 PagedPlan paged_plan(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_kv, int heads, int group, int head_dim,
                      int64_t window)
 {
@@ -717,7 +723,10 @@ PagedPlan paged_plan(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_k
         k.counter = take(4 * (uint64_t)k.grid * parts);
         k.part = take(2 * (uint64_t)k.grid * k.rows * (head_dim + 2) * 4);
     };
-    const bool many = rows > 64;
+    // tokens a job reads
+    const int64_t reach = window > 0 && window + max_q < max_kv ? window + max_q : max_kv;
+    const bool wide = head_dim == 256;
+    const bool many = rows > (wide ? 32 : 64) && (rows > 128 || reach > (wide ? 1024 : 4096));
     if (!many || batch > 1) {
         p.few.rows = many || rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
         p.few.row_hi = many ? 16 : INT32_MAX;
@@ -730,9 +739,8 @@ PagedPlan paged_plan(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_k
         // tokens 10.3 / 32.8 us, by shares 16.4 / 47.2; eight of 4096 to 8192
         // tokens 40.6 us, by shares 48.7.
         const int64_t row_tiles = (rows + p.few.rows - 1) / p.few.rows;
-        const int64_t reach = window > 0 && window + max_q < max_kv ? window + max_q : max_kv;  // tokens a job reads
         const int64_t tiles = (reach + kFewT - 1) / kFewT + (reach < max_kv ? 1 : 0);
-        const int64_t jobs = batch * heads * row_tiles, most = jobs <= (head_dim == 256 ? 4 : 8) ? 16 : 8;
+        const int64_t jobs = batch * heads * row_tiles, most = jobs <= (wide ? 4 : 8) ? 16 : 8;
         if (!many && jobs > 0 && jobs <= p.few.grid) {
             int split = 1;
             while (split < most && 2 * split * jobs <= p.few.grid && split < tiles) split *= 2;
@@ -775,12 +783,12 @@ cudaError_t launch_paged(const PagedArgs &args, const PagedPlan &p, int head_dim
     };
     PagedArgs a = share(p.few);
     a.job_cost = kJobCostFew;
-    a.min_units = kJobCostFew + 2;
+    a.min_units = 2;
     cudaError_t e;
     if (p.many.grid) {
         PagedArgs b = share(p.many);
         b.job_cost = kJobCostMany;
-        b.min_units = kJobCostMany + 4;
+        b.min_units = 3;
         e = launch_plan_many(b, a, head_dim, p.few.grid > 0, s);
         if (e == cudaSuccess) e = launch_paged_many(b, head_dim, s);
         if (!p.few.grid) return e;
