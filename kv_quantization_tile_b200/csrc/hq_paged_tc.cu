@@ -247,9 +247,11 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
         prefetch_map(&vmap);
     }
     pdl_wait();
-    // segment i (whether there is one), and this warp's leave of it
-    auto segment = [&](uint32_t i) -> bool {
-        return __all_sync(FULL, wait(seg_full(i % kSegments), (i / kSegments) & 1u)) && s_seg[i % kSegments].valid;
+    // segment i (whether there is one; `ok` turns false if the wait gave up),
+    // and this warp's leave of it
+    auto segment = [&](uint32_t i, bool &ok) -> bool {
+        if (!__all_sync(FULL, wait(seg_full(i % kSegments), (i / kSegments) & 1u))) ok = false;
+        return ok && s_seg[i % kSegments].valid;
     };
     auto leave = [&](uint32_t i) {
         __syncwarp();
@@ -293,7 +295,8 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
             if (lane == 0) mbar_arrive(q_full(t));
         };
         uint32_t i = 0;
-        bool more = segment(0);
+        bool ok = true, more = segment(0, ok);
+        if (named_any(9 + t, 256, !ok)) more = false;  // the MMA tile's warps go on together or not at all
         if (more) {
             copy_queries(s_seg[0]);
             hand_queries();
@@ -308,7 +311,6 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                 seen_range(a, s, j, j, rlo, rhi);
             }
             float m = -INFINITY, l = 0.0f;
-            bool ok = true;
             for (int n = 0; n < count; n++, g++) {
                 const int b = NT == 2 ? t : (int)(g & 1u);
                 const uint32_t par = NT == 2 ? g & 1u : (g >> 1) & 1u;
@@ -324,7 +326,7 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                 // the last scores are there, so the queries are free: the next
                 // segment's take their place
                 if (n + 1 == count) {
-                    more = segment(i + 1);
+                    more = segment(i + 1, ok);
                     if (more && ok) copy_queries(s_seg[(i + 1) % kSegments]);
                 }
                 const uint32_t mine = ts + (uint32_t)(hf * (T / 2));  // this half's scores, then its weights
@@ -558,14 +560,14 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
             // The warp walks as one, so addresses stay in uniform registers;
             // one elected lane issues (always the same one: a commit covers
             // the products of its own thread).
-            if (segment(0)) {
+            bool ok = true;
+            if (segment(0, ok)) {
                 constexpr uint32_t ID_S = make_idesc_bf16(128, T);
                 constexpr uint32_t ID_O = make_idesc_bf16(128, D) | (1u << 16);  // V is token-major: B not K-major
                 const bool one = elect_one();
                 const uint64_t qd = swizzled_desc(sq, 16, 1024), kd = swizzled_desc(ring, 16, 1024),
                                vd = swizzled_desc(ring, T * 128, 1024);
                 uint32_t slot = 0, phase = 0, g = 0, seg = 0;
-                bool ok = true;
                 auto take = [&]() -> uint32_t {  // the next tile of the ring, landed
                     ok = ok && wait(kv_full(slot), phase);
                     const uint32_t s = slot;
@@ -645,7 +647,7 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                         if (NT == 2 && more) commit(kv_empty(k));
                     }
                     seg++;
-                } while (ok && segment(seg));
+                } while (ok && segment(seg, ok));
             }
         } else if ((warp & 3) == 1) {
             // -------------------------------------------- loads
@@ -699,7 +701,7 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                     phase ^= 1u;
                 }
             };
-            for (uint32_t i = 0; ok && segment(i); i++) {
+            for (uint32_t i = 0; ok && segment(i, ok); i++) {
                 x = s_seg[i % kSegments];
                 leave(i);
                 uint32_t here = page_of(0), next = page_of(1);
