@@ -723,8 +723,8 @@ PagedPlan paged_plan(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_k
         k.counter = take(4 * (uint64_t)k.grid * parts);
         k.part = take(2 * (uint64_t)k.grid * k.rows * (head_dim + 2) * 4);
     };
-    // tokens a job reads
-    const int64_t reach = window > 0 && window + max_q < max_kv ? window + max_q : max_kv;
+    // tokens a job reads (any window up to INT64_MAX; max_q <= 2^30)
+    const int64_t reach = window > 0 && window < max_kv - max_q ? window + max_q : max_kv;
     const bool wide = head_dim == 256;
     const bool many = rows > (wide ? 32 : 64) && (rows > 128 || reach > (wide ? 1024 : 4096));
     if (!many || batch > 1) {
@@ -739,8 +739,11 @@ PagedPlan paged_plan(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_k
         // tokens 10.3 / 32.8 us, by shares 16.4 / 47.2; eight of 4096 to 8192
         // tokens 40.6 us, by shares 48.7.
         const int64_t row_tiles = (rows + p.few.rows - 1) / p.few.rows;
-        const int64_t tiles = (reach + kFewT - 1) / kFewT + (reach < max_kv ? 1 : 0);
-        const int64_t jobs = batch * heads * row_tiles, most = jobs <= (wide ? 4 : 8) ? 16 : 8;
+        // a window cuts one tile more than its length, but never more than there
+        // are: a plan with a window then fits the workspace of one without
+        const int64_t all = (max_kv + kFewT - 1) / kFewT, cut = (reach + kFewT - 1) / kFewT + 1;
+        const int64_t tiles = cut < all ? cut : all;
+        const int64_t jobs = many ? 0 : batch * heads * row_tiles, most = jobs <= (wide ? 4 : 8) ? 16 : 8;
         if (!many && jobs > 0 && jobs <= p.few.grid) {
             int split = 1;
             while (split < most && 2 * split * jobs <= p.few.grid && split < tiles) split *= 2;

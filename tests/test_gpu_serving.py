@@ -242,6 +242,12 @@ def test_attention_window(d, q_lens, kv_lens, window):
     run_attention(q_lens, kv_lens, 1, 4, d, 16, window=window, seed=window)
 
 
+@pytest.mark.parametrize("q_lens,max_kv,window", [([1, 1], 16384, 16382), ([1, 1], 16384, (1 << 63) - 1),
+                                                  ([150, 2], 4096, (1 << 63) - 1), ([150, 2], 4096, 1 << 31)])
+def test_attention_windows_about_the_bounds(q_lens, max_kv, window):
+    run_attention(q_lens, [400, 77], 8, 4, 128, 64, window=window, max_kv=max_kv)
+
+
 @pytest.mark.parametrize("q_lens,kv_lens", [([1, 4], [90, 33]), ([100, 70], [300, 20])])
 @pytest.mark.parametrize("window", [0, 40])
 def test_attention_without_causal_mask(q_lens, kv_lens, window):

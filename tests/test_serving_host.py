@@ -199,6 +199,23 @@ def test_a_workspace_for_larger_bounds_serves_smaller_calls():
         assert size(small) <= size(big), (small, big, d, heads, group)
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="ends at the launch, which has to fail")
+def test_any_window_fits_the_workspace_of_the_bounds():
+    rng = np.random.default_rng(1)
+    for n in range(6000):
+        d, heads, group = int(rng.choice([64, 128, 256])), int(rng.integers(1, 33)), int(rng.integers(1, 9))
+        batch, max_q = int(2 ** rng.uniform(0, 6)), int(2 ** rng.uniform(0, 7))
+        max_kv = int(2 ** rng.integers(8, 17)) if n % 2 else int(2 ** rng.uniform(0, 17))
+        size = hq.hq_paged_attention_workspace_bytes(batch, batch * max_q, max_q, max_kv, heads, d, group)
+        hs, ts = d, d * heads * group
+        by = dict(q=rows(ts=ts, hs=hs), out=rows(ts=ts, hs=hs), batch=batch, tokens=batch * max_q, max_q=max_q, max_kv=max_kv,
+                  group=group, ws_bytes=size, pg=pages(heads=heads, head_dim=d, page_stride=16 * d * heads, head_stride=16 * d,
+                                                       slot_stride=d))
+        for window in (1, max_kv // 2, max_kv - max_q, max_kv - max_q - 1, max_kv, 1 << 31, (1 << 63) - 1):
+            if window >= 0:
+                assert attention(window=window, **by) == hq.HQ_ERR_CUDA, (batch, max_q, max_kv, heads, group, d, window)
+
+
 def test_cpu_tensors_and_wrong_shapes_are_refused():
     """The binding refuses what it could only turn into a bad device access."""
     x = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
