@@ -525,6 +525,24 @@ int hq_paged_attention(const hq_rows *q, const int32_t *q_start, const int32_t *
                        int causal, int64_t window, const hq_rows *out, float *lse, void *workspace,
                        uint64_t workspace_bytes, void *stream, int32_t *d_status);
 
+/* Testing hook for failure detection (no counterpart on the pages):
+ * hq_paged_attention in which thread block 0 withholds one hand-over between
+ * its warps, so that the bounded waits for it run out (0.5 s each):
+ *   kind 1  copy number `stalled` of its walk from the pages (a tile of K and V
+ *           together in the kernel for few rows, of either alone in the one for
+ *           many)
+ *   kind 2  the notice that the product of its tile number `stalled` with V is
+ *           complete (the kernel for many rows; the other has none)
+ * The block raises HQ_ST_TIMEOUT, leaves with no copy or product in flight,
+ * frees its tensor memory and returns; the output is invalid, the device stays
+ * usable.  Not for production use. */
+int hq_test_paged_attention_stalled(const hq_rows *q, const int32_t *q_start, const int32_t *kv_len, int64_t batch,
+                                    int64_t tokens, int64_t max_q, int64_t max_kv, int group, const hq_pages *pages,
+                                    const int32_t *table, int64_t table_width, int64_t table_stride, float scale,
+                                    int causal, int64_t window, const hq_rows *out, float *lse, void *workspace,
+                                    uint64_t workspace_bytes, void *stream, int32_t *d_status, int kind,
+                                    int stalled);
+
 /* Join two partial attention results over disjoint sets of cached tokens:
  *   out = (w_a a + w_b b) / (w_a + w_b),  w = exp(lse - max(lse_a, lse_b)),
  *   lse = log(exp(lse_a) + exp(lse_b))

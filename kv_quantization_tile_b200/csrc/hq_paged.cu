@@ -219,6 +219,7 @@ paged_few_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, co
     if (!work) return;
     __syncthreads();
     uint32_t stage = 0, phase = 0;
+    int left = blockIdx.x == 0 && a.stall_kind == kStallCopy ? a.stall : -1;  // tiles before the withheld one
     bool ok = true;  // a wait that gave up ends the loops; results are invalid then
     auto advance = [&]() {
         if (++stage == STAGES) {
@@ -255,12 +256,13 @@ paged_few_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, co
                 const uint32_t n = __popc(__ballot_sync(FULL, mine));
                 if (lane == 0) mbar_expect(full(stage), n * (uint32_t)box * 256u);
                 __syncwarp();
-                if (mine) {
+                if (mine && left != 0) {
                     const uint32_t dst = ring0 + stage * 2 * TILE + (uint32_t)(col * T * 128 + pg * box * 128);
                     const int at = tok & (page_rows - 1);
                     tma_page(dst, &kmap, full(stage), col * 64, at, w.h, (int)page);
                     tma_page(dst + TILE, &vmap, full(stage), col * 64, at, w.h, (int)page);
                 }
+                if (left >= 0) left--;
                 page = next;
                 advance();
             }

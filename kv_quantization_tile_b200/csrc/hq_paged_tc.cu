@@ -241,6 +241,9 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
         s_fail = 1;
         return false;
     };
+    // the same for a warp that walks as one: its lanes go on together or not at
+    // all (the clocks by which a wait gives up are read lane by lane)
+    auto wait_as_one = [&](uint32_t bar, uint32_t parity) -> bool { return __all_sync(FULL, wait(bar, parity)); };
 
     if (warp == 2 && lane == 0) {
         prefetch_map(&kmap);
@@ -250,7 +253,7 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
     // segment i (whether there is one; `ok` turns false if the wait gave up),
     // and this warp's leave of it
     auto segment = [&](uint32_t i, bool &ok) -> bool {
-        if (!__all_sync(FULL, wait(seg_full(i % kSegments), (i / kSegments) & 1u))) ok = false;
+        if (!wait_as_one(seg_full(i % kSegments), (i / kSegments) & 1u)) ok = false;
         return ok && s_seg[i % kSegments].valid;
     };
     auto leave = [&](uint32_t i) {
@@ -569,7 +572,7 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                                vd = swizzled_desc(ring, T * 128, 1024);
                 uint32_t slot = 0, phase = 0, g = 0, seg = 0;
                 auto take = [&]() -> uint32_t {  // the next tile of the ring, landed
-                    ok = ok && wait(kv_full(slot), phase);
+                    ok = ok && wait_as_one(kv_full(slot), phase);
                     const uint32_t s = slot;
                     if (++slot == STAGES) {
                         slot = 0;
@@ -601,13 +604,13 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
 #pragma unroll
                             for (int i = i0; i < i1; i++)
                                 umma_bf16_ts(d, p + h * (T / 2) + 8 * i, v + (h * (T / 32) + i) * 128, ID_O, add || h + i > 0);
-                        if (last) umma_commit(o_full(t));
+                        if (last && !(blockIdx.x == 0 && a.stall_kind == kStallProduct && (int)g == a.stall)) umma_commit(o_full(t));
                     }
                 };
                 do {
                     const uint32_t k0 = take();
                     for (int t = 0; t < NT && ok; t++) {
-                        ok = wait(q_full(t), seg & 1u);
+                        ok = wait_as_one(q_full(t), seg & 1u);
                         if (!ok) break;
                         tc_fence_after();
                         scores(t, NT == 2 ? t : (int)(g & 1u), k0);
@@ -630,12 +633,12 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                             const int b = NT == 2 ? t : (int)(g & 1u);
                             const uint32_t par = NT == 2 ? g & 1u : (g >> 1) & 1u;
                             if (T == 128) {  // the first 32 weights of either half
-                                ok = wait(p_half(b), par);
+                                ok = wait_as_one(p_half(b), par);
                                 if (!ok) break;
                                 tc_fence_after();
                                 outputs(t, b, v, 0, 2, j > 0, false);
                             }
-                            ok = wait(p_full(b), par);
+                            ok = wait_as_one(p_full(b), par);
                             if (!ok) break;
                             tc_fence_after();
                             if (T == 128) outputs(t, b, v, 2, 4, true, true);
@@ -654,6 +657,7 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
             const int page_rows = 1 << a.page_shift, box = page_rows < T ? page_rows : T;
             const int col = lane % (D / 64), pg = lane / (D / 64);
             uint32_t slot = 0, phase = 0, fixes = 0;
+            int left = blockIdx.x == 0 && a.stall_kind == kStallCopy ? a.stall : -1;  // copies before the withheld one
             bool ok = true;
             // this lane's page of a tile (past the pool, where TMA fills zeros,
             // for a number outside it); read a tile ahead of its use
@@ -669,8 +673,7 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                 return page;
             };
             auto load = [&](int n, bool is_v, uint32_t page) {
-                ok = ok && wait(kv_empty(slot), phase ^ 1u);
-                ok = __all_sync(FULL, ok);
+                ok = ok && wait_as_one(kv_empty(slot), phase ^ 1u);
                 if (!ok) return;
                 const int tok0 = (x.tile + n) * T, tok = tok0 + pg * box;
                 const uint32_t dst = ring + slot * C::TILE;
@@ -681,11 +684,13 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                 const uint32_t boxes = __popc(__ballot_sync(FULL, mine));
                 if (lane == 0) mbar_expect(bar, boxes * (uint32_t)box * 128u);
                 __syncwarp();
-                if (mine)
+                if (mine && left != 0)
                     tma_page(dst + (uint32_t)(col * T * 128 + pg * box * 128), is_v ? &vmap : &kmap, bar, col * 64,
                              tok & (page_rows - 1), x.h, (int)page);
+                if (left >= 0) left--;
                 if (fix) {
-                    ok = wait(fix_bar, fixes & 1u);
+                    ok = wait_as_one(fix_bar, fixes & 1u);
+                    if (!ok) return;
                     fixes++;
                     for (int e = lane; e < T * (D / 8); e += 32) {
                         const int r = e / (D / 8), c = e % (D / 8);
@@ -722,7 +727,7 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
             SegWalk<T, RT> w;
             bool go = w.begin(a);
             for (uint32_t i = 0;; i++) {
-                if (!__all_sync(FULL, wait(seg_empty(i % kSegments), ((i / kSegments) & 1u) ^ 1u))) break;
+                if (!wait_as_one(seg_empty(i % kSegments), ((i / kSegments) & 1u) ^ 1u)) break;
                 if (lane == 0) {
                     Segment x{};
                     x.valid = go;

@@ -238,11 +238,11 @@ int hq_paged_attention_workspace_bytes(int64_t batch, int64_t tokens, int64_t ma
     return HQ_OK;
 }
 
-int hq_paged_attention(const hq_rows *q, const int32_t *q_start, const int32_t *kv_len, int64_t batch, int64_t tokens,
-                       int64_t max_q, int64_t max_kv, int group, const hq_pages *pages, const int32_t *table,
-                       int64_t table_width, int64_t table_stride, float scale, int causal, int64_t window,
-                       const hq_rows *out, float *lse, void *workspace, uint64_t workspace_bytes, void *stream,
-                       int32_t *d_status)
+static int paged_attention(const hq_rows *q, const int32_t *q_start, const int32_t *kv_len, int64_t batch, int64_t tokens,
+                           int64_t max_q, int64_t max_kv, int group, const hq_pages *pages, const int32_t *table,
+                           int64_t table_width, int64_t table_stride, float scale, int causal, int64_t window,
+                           const hq_rows *out, float *lse, void *workspace, uint64_t workspace_bytes, void *stream,
+                           int32_t *d_status, int stall_kind, int stall)
 {
     int rc = check_pages(pages);
     if (rc) return rc;
@@ -285,8 +285,31 @@ int hq_paged_attention(const hq_rows *q, const int32_t *q_start, const int32_t *
     a.q_mode = scale == 0.0f ? 2 : scale < 0.0f ? 1 : 0;
     a.causal = causal != 0;
     a.window = (int)(window > INT32_MAX ? 0 : window);  // wider than any cache: all
+    a.stall_kind = stall_kind;
+    a.stall = stall;
     a.status = d_status;
     return launch_paged(a, p, d, workspace, (cudaStream_t)stream) == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
+}
+
+int hq_paged_attention(const hq_rows *q, const int32_t *q_start, const int32_t *kv_len, int64_t batch, int64_t tokens,
+                       int64_t max_q, int64_t max_kv, int group, const hq_pages *pages, const int32_t *table,
+                       int64_t table_width, int64_t table_stride, float scale, int causal, int64_t window,
+                       const hq_rows *out, float *lse, void *workspace, uint64_t workspace_bytes, void *stream,
+                       int32_t *d_status)
+{
+    return paged_attention(q, q_start, kv_len, batch, tokens, max_q, max_kv, group, pages, table, table_width, table_stride,
+                           scale, causal, window, out, lse, workspace, workspace_bytes, stream, d_status, kStallNone, 0);
+}
+
+int hq_test_paged_attention_stalled(const hq_rows *q, const int32_t *q_start, const int32_t *kv_len, int64_t batch,
+                                    int64_t tokens, int64_t max_q, int64_t max_kv, int group, const hq_pages *pages,
+                                    const int32_t *table, int64_t table_width, int64_t table_stride, float scale, int causal,
+                                    int64_t window, const hq_rows *out, float *lse, void *workspace,
+                                    uint64_t workspace_bytes, void *stream, int32_t *d_status, int kind, int stalled)
+{
+    if ((kind != kStallCopy && kind != kStallProduct) || stalled < 0) return HQ_ERR_ARG;
+    return paged_attention(q, q_start, kv_len, batch, tokens, max_q, max_kv, group, pages, table, table_width, table_stride,
+                           scale, causal, window, out, lse, workspace, workspace_bytes, stream, d_status, kind, stalled);
 }
 
 int hq_attention_merge(const hq_rows *a, const float *lse_a, const hq_rows *b, const float *lse_b, int64_t tokens,

@@ -36,7 +36,8 @@ EXPORTS = ["hq_error_string", "hq_version", "hq_rate_constant", "hq_tile_bound_w
            "hq_min_slot_words", "hq_fixed_slot_words", "hq_encode_fixed", "hq_kv_encode_fixed",
            "hq_decode_gemm_int8_workspace_bytes", "hq_decode_gemm_int8", "hq_decode_gemm_fp8",
            "hq_stream_stats", "hq_kv_attention_lse", "hq_rope_frequencies", "hq_rope_table", "hq_rope",
-           "hq_kv_append", "hq_paged_attention_workspace_bytes", "hq_paged_attention", "hq_attention_merge"]
+           "hq_kv_append", "hq_paged_attention_workspace_bytes", "hq_paged_attention", "hq_attention_merge",
+           "hq_test_paged_attention_stalled"]
 HQ_ROPE_PLAIN, HQ_ROPE_LINEAR, HQ_ROPE_NTK, HQ_ROPE_BANDS, HQ_ROPE_YARN = range(5)
 HQ_ROPE_HALF, HQ_ROPE_INTERLEAVED = 0, 1
 ROPE_LAYOUTS = {"half": HQ_ROPE_HALF, "interleaved": HQ_ROPE_INTERLEAVED}
@@ -130,6 +131,9 @@ _SIGS = {
     "hq_paged_attention": (_i32, [ctypes.POINTER(hq_rows), _vp, _vp, _i64, _i64, _i64, _i64, _i32,
                                   ctypes.POINTER(hq_pages), _vp, _i64, _i64, _f32, _i32, _i64,
                                   ctypes.POINTER(hq_rows), _vp, _vp, _u64, _vp, _vp]),
+    "hq_test_paged_attention_stalled": (_i32, [ctypes.POINTER(hq_rows), _vp, _vp, _i64, _i64, _i64, _i64, _i32,
+                                               ctypes.POINTER(hq_pages), _vp, _i64, _i64, _f32, _i32, _i64,
+                                               ctypes.POINTER(hq_rows), _vp, _vp, _u64, _vp, _vp, _i32, _i32]),
     "hq_attention_merge": (_i32, [ctypes.POINTER(hq_rows), _vp, ctypes.POINTER(hq_rows), _vp, _i64, _i32, _i32,
                                   ctypes.POINTER(hq_rows), _vp, _vp]),
     "hq_kv_attention": (_i32, [ctypes.POINTER(hq_stream), ctypes.POINTER(hq_stream), _i64, _i64, _i32, _i32,
@@ -640,6 +644,22 @@ def hq_paged_attention(q, q_start, kv_len, pages: Pages, page_table, scale: floa
     heads * group]."""
     _hq_torch.attention(q, q_start, kv_len, pages.k, pages.v, page_table, scale, out, workspace, max_q, max_kv, causal,
                         window, lse, status, _handle(stream))
+    return out
+
+
+def hq_test_paged_attention_stalled(q, q_start, kv_len, pages: Pages, page_table, scale: float, out, workspace,
+                                    max_q: int, max_kv: int, kind: int, stalled: int, status=None, stream=None):
+    """hq_paged_attention with one hand-over inside a block withheld (a
+    failure-detection test hook; kind 1: copy number `stalled`, 2: the notice of
+    tile `stalled`'s product): the bounded waits run out and HQ_ST_TIMEOUT is raised."""
+    rows = lambda t: hq_rows(_ptr(t), HQ_BF16 if t.dtype == torch.bfloat16 else HQ_F32, *t.stride()[:2])  # noqa: E731
+    n, heads, size, d = pages.k.shape
+    pool = hq_pages(_ptr(pages.k), _ptr(pages.v), n, size, heads, d, *pages.k.stride()[:3])
+    _check(_lib.hq_test_paged_attention_stalled(
+        ctypes.byref(rows(q)), _ptr(q_start), _ptr(kv_len), kv_len.numel(), q.shape[0], max_q, max_kv,
+        q.shape[1] // heads, ctypes.byref(pool), _ptr(page_table), page_table.shape[1], page_table.stride(0), scale, 1, 0,
+        ctypes.byref(rows(out)), None, _ptr(workspace), workspace.numel(), _stream_handle(stream), _ptr(status), kind,
+        stalled), "hq_test_paged_attention_stalled")
     return out
 
 
