@@ -227,6 +227,9 @@ paged_few_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, co
             phase ^= 1u;
         }
     };
+    auto land = [&]() {  // (the load warp) no copy is left in flight
+        for (uint32_t s = 0; s < STAGES; s++) mbar_wait(full(s), s < stage ? phase : phase ^ 1u);
+    };
     do {
         const int r0 = w.rt * RT, nr = min(RT, w.s.rows - r0);
         const int end = w.first + w.count;
@@ -266,8 +269,8 @@ paged_few_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, co
                 page = next;
                 advance();
             }
-            if (!ok)  // let the copies in flight land
-                for (uint32_t s = 0; s < STAGES; s++) mbar_wait(full(s), s < stage ? phase : phase ^ 1u);
+            // before another use of the ring, where the consumers may have given up
+            if (CLUSTER || !ok) land();
             __syncthreads();  // (A) the ring holds the consumers' outputs until (B)
             if constexpr (!CLUSTER) ok = !__syncthreads_or(!ok);
         } else {
@@ -535,6 +538,8 @@ paged_few_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, co
             return;
         }
     } while (ok && w.next(a));
+    if constexpr (!CLUSTER)
+        if (warp == W && !ok) land();
 }
 
 // ------------------------------------------------------------ join

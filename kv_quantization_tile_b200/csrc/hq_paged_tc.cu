@@ -187,7 +187,7 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
     using C = Many<D>;
     constexpr int NT = C::NT, RT = C::RT, T = C::T, STAGES = C::STAGES;
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t s_bar[2 * STAGES + NT * 2 + 6 + 1 + 2 * kSegments];
+    __shared__ __align__(8) uint64_t s_bar[2 * STAGES + NT * 2 + 6 + 2 + 2 * kSegments];
     __shared__ Segment s_seg[kSegments];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_fail;
@@ -205,8 +205,9 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
     auto p_full = [&](int b) { return bar0 + 8u * (uint32_t)(2 * STAGES + 2 * NT + 2 + b); };
     auto p_half = [&](int b) { return bar0 + 8u * (uint32_t)(2 * STAGES + 2 * NT + 4 + b); };  // the first 32 weights of either half
     const uint32_t fix_bar = bar0 + 8u * (uint32_t)(2 * STAGES + 2 * NT + 6);
-    auto seg_full = [&](uint32_t k) { return fix_bar + 8u * (1 + k); };
-    auto seg_empty = [&](uint32_t k) { return fix_bar + 8u * (1 + kSegments + k); };
+    const uint32_t done_bar = fix_bar + 8u;  // the block's last product
+    auto seg_full = [&](uint32_t k) { return fix_bar + 8u * (2 + k); };
+    auto seg_empty = [&](uint32_t k) { return fix_bar + 8u * (2 + kSegments + k); };
 
     if (warp == 0) tmem_alloc(smem_u32(&s_tmem), 512);
     if (tid == 0) {
@@ -225,6 +226,7 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
             mbar_init(p_half(b), 8);
         }
         mbar_init(fix_bar, 1);
+        mbar_init(done_bar, 1);
         for (int k = 0; k < kSegments; k++) {
             mbar_init(seg_full(k), 1);
             mbar_init(seg_empty(k), 8 * NT + 2);  // the softmax warps, products, loads
@@ -557,6 +559,7 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                 a.lse[tok * (a.heads * a.group) + head] = lt == 0.0f ? -INFINITY : fmaf(mt, 0.693147180559945309f, logf(lt));
             leave(i);
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");  // queries copied ahead for a segment that was given up
     } else {
         if ((warp & 3) == 0) {
             // -------------------------------------------- products
@@ -651,6 +654,9 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                     }
                     seg++;
                 } while (ok && segment(seg, ok));
+                // no product is left running, whoever gave up
+                commit(done_bar);
+                wait_as_one(done_bar, 0);
             }
         } else if ((warp & 3) == 1) {
             // -------------------------------------------- loads
@@ -690,8 +696,8 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                 if (left >= 0) left--;
                 if (fix) {
                     ok = wait_as_one(fix_bar, fixes & 1u);
-                    if (!ok) return;
                     fixes++;
+                    if (!ok) return;
                     for (int e = lane; e < T * (D / 8); e += 32) {
                         const int r = e / (D / 8), c = e % (D / 8);
                         if (tok0 + r < x.lo || tok0 + r >= x.hi)
@@ -719,9 +725,9 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                     next = after;
                 }
             }
-            // after a wait that gave up, let the copies in flight land
-            if (!ok)
-                for (int s = 0; s < STAGES; s++) mbar_wait(kv_full(s), s < (int)slot ? phase : phase ^ 1u);
+            // no copy is left in flight, whoever gave up
+            for (int s = 0; s < STAGES; s++) mbar_wait(kv_full(s), s < (int)slot ? phase : phase ^ 1u);
+            if (!ok && fixes) mbar_wait(fix_bar, (fixes - 1u) & 1u);
         } else {
             // -------------------------------------------- jobs
             SegWalk<T, RT> w;

@@ -67,3 +67,12 @@ def test_a_page_copy_that_never_lands_shares_of_few_rows(d, stalled):
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_a_page_copy_that_never_lands_chunks(d, stalled):
     run_stalled([1021], [2043], 8, 4, d, COPY, stalled)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("q_lens,kv_lens,kvh,group,last", [([1], [4096], 2, 4, 3), ([1] * 60, [600] * 60, 8, 2, 9),
+                                                           ([1021], [2043], 8, 4, 17)])
+def test_a_last_page_copy_that_never_lands(d, q_lens, kv_lens, kvh, group, last):
+    """The load warp has issued all its copies when the others give up: it still
+    stays until they have landed."""
+    run_stalled(q_lens, kv_lens, kvh, group, d, COPY, last)
