@@ -321,7 +321,7 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                 const uint32_t par = NT == 2 ? g & 1u : (g >> 1) & 1u;
                 const uint32_t ts = tmem + lanes + C::S_COL + (uint32_t)(b * T);
                 constexpr int NC = T / 64;  // chunks of 32 columns of this half
-                ok = wait(s_full(b), par);
+                ok = wait(s_full(b), par) && ok;  // (a wait for O that gave up in the tile before counts)
                 // Every product with V is waited for in turn (a barrier's phase can
                 // only be told from the one before it).  With two MMA tiles S comes
                 // after that product anyway; with one, S runs ahead of it.
@@ -400,7 +400,7 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                     if (grow) m = top;
                     l *= f;
                     if (n > 0) {  // rescale O: the product before this one is complete
-                        ok = wait(o_full(t), (g - 1u) & 1u);  // (a failure is met at the next vote)
+                        ok = wait(o_full(t), (g - 1u) & 1u);  // (a failure is met at the next tile's vote)
                         ok = __all_sync(FULL, ok);
                         tc_fence_after();
 #pragma unroll 1
