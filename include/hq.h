@@ -531,8 +531,10 @@ int hq_paged_attention(const hq_rows *q, const int32_t *q_start, const int32_t *
  *   kind 1  copy number `stalled` of its walk from the pages (a tile of K and V
  *           together in the kernel for few rows, of either alone in the one for
  *           many)
- *   kind 2  the notice that the product of its tile number `stalled` with V is
- *           complete (the kernel for many rows; the other has none)
+ *   kind 2  from its tile number `stalled` on, the notice that the product with
+ *           V is complete (the kernel for many rows; the other has none).  A
+ *           notice is told from the one two before by nothing: an even number,
+ *           where the head size is 64 or 128 and the job has an odd number of tiles
  * The block raises HQ_ST_TIMEOUT, leaves with no copy or product in flight,
  * frees its tensor memory and returns; the output is invalid, the device stays
  * usable.  Not for production use. */

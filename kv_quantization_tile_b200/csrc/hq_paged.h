@@ -88,7 +88,7 @@ struct PagedArgs {
     int grid, min_units;     // blocks; least units of work a block takes
     int job_cost;            // what a job costs beside its tiles, in tiles
     int split, row_tiles;    // clusters (no plan): blocks of a job, row tiles of the longest sequence
-    int stall_kind, stall;   // test hook: what block 0 withholds, and of which tile or copy
+    int stall_kind, stall;   // test hook: what block 0 withholds: this copy, or the products' notices from this tile on
     int32_t *status;
 };
 constexpr int kStallNone = 0, kStallCopy = 1, kStallProduct = 2;

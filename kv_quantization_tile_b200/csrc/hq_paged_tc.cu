@@ -607,7 +607,7 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
 #pragma unroll
                             for (int i = i0; i < i1; i++)
                                 umma_bf16_ts(d, p + h * (T / 2) + 8 * i, v + (h * (T / 32) + i) * 128, ID_O, add || h + i > 0);
-                        if (last && !(blockIdx.x == 0 && a.stall_kind == kStallProduct && (int)g == a.stall)) umma_commit(o_full(t));
+                        if (last && !(blockIdx.x == 0 && a.stall_kind == kStallProduct && (int)g >= a.stall)) umma_commit(o_full(t));
                     }
                 };
                 do {

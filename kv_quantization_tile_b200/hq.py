@@ -650,8 +650,8 @@ def hq_paged_attention(q, q_start, kv_len, pages: Pages, page_table, scale: floa
 def hq_test_paged_attention_stalled(q, q_start, kv_len, pages: Pages, page_table, scale: float, out, workspace,
                                     max_q: int, max_kv: int, kind: int, stalled: int, status=None, stream=None):
     """hq_paged_attention with one hand-over inside a block withheld (a
-    failure-detection test hook; kind 1: copy number `stalled`, 2: the notice of
-    tile `stalled`'s product): the bounded waits run out and HQ_ST_TIMEOUT is raised."""
+    failure-detection test hook; kind 1: copy number `stalled`, 2: the notices
+    of products from tile `stalled` on): the bounded waits run out and HQ_ST_TIMEOUT is raised."""
     rows = lambda t: hq_rows(_ptr(t), HQ_BF16 if t.dtype == torch.bfloat16 else HQ_F32, *t.stride()[:2])  # noqa: E731
     n, heads, size, d = pages.k.shape
     pool = hq_pages(_ptr(pages.k), _ptr(pages.v), n, size, heads, d, *pages.k.stride()[:3])

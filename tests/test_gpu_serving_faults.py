@@ -80,7 +80,7 @@ def test_a_last_page_copy_that_never_lands(d, q_lens, kv_lens, kvh, group, last)
 
 @pytest.mark.parametrize("grow", [False, True])
 @pytest.mark.parametrize("d,stalled", [(64, 0), (64, 4), (128, 0), (128, 4), (256, 0), (256, 5), (128, 8)])
-def test_a_product_whose_notice_never_comes(d, stalled, grow):
+def test_products_whose_notices_never_come(d, stalled, grow):
     """Waited for where the output is rescaled (keys that grow), or at the end of
-    the job; a failure in the first place holds until the warps next vote."""
+    the job (nine tiles); a failure in the first place holds until the warps next vote."""
     run_stalled([1021], [2043], 8, 4, d, PRODUCT, stalled, grow)
