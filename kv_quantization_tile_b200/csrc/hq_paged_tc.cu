@@ -732,8 +732,19 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
             // -------------------------------------------- jobs
             SegWalk<T, RT> w;
             bool go = w.begin(a);
-            for (uint32_t i = 0;; i++) {
-                if (!wait_as_one(seg_empty(i % kSegments), ((i / kSegments) & 1u) ^ 1u)) break;
+            int64_t tiles = 0;  // of the segments so far
+            // The place of the segment four back: that one may last longer than any
+            // one wait, so this one gives up where another role has (each waits for
+            // a tile at most), and after as many limits as there were tiles.
+            auto place = [&](uint32_t i) -> bool {
+                for (int64_t left = tiles;; left--) {
+                    if (__all_sync(FULL, mbar_wait(seg_empty(i % kSegments), ((i / kSegments) & 1u) ^ 1u))) return true;
+                    if (left <= 0 || __any_sync(FULL, s_fail)) break;
+                }
+                s_fail = 1;
+                return false;
+            };
+            for (uint32_t i = 0; place(i); i++) {
                 if (lane == 0) {
                     Segment x{};
                     x.valid = go;
@@ -761,6 +772,7 @@ paged_many_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap kmap, c
                 }
                 __syncwarp();
                 if (!go) break;
+                tiles += w.count;
                 go = w.next(a);
             }
         }
