@@ -215,10 +215,20 @@ struct SegWalk {
             if (++h == a.heads) {
                 h = 0;
                 bool bad;
-                do {
-                    if (++b >= a.batch) return false;
+                if (++b >= a.batch) return false;
+                s = load_seq(a, b, bad);
+                if (s.rows == 0) {
+                    // the sequence with work in it that begins at this unit: the last
+                    // that begins here (one by one, millions of empty ones would
+                    // outlast the other warps' waits)
+                    int above = a.batch - 1;
+                    while (b < above) {
+                        const int mid = (int)(((int64_t)b + above + 1) >> 1);
+                        if (a.prefix[mid] <= job) b = mid;
+                        else above = mid - 1;
+                    }
                     s = load_seq(a, b, bad);
-                } while (s.rows == 0);
+                }
                 nrt = (s.rows + RT - 1) / RT;
             }
         }

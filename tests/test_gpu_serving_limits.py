@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from kv_quantization_tile_b200 import hq
-from serving_util import assert_within, attend, randn, starts
+from serving_util import assert_within, attend, make_cache, randn, starts
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -40,5 +40,32 @@ def test_a_segment_longer_than_any_wait():
     n = [page] * long + [100] * short
     ref, ref_lse, tol, _, tol_l = attend(q, [k[1, 0, :m, None] for m in n], [v[1, 0, :m, None] for m in n], [q_len] * batch,
                                          1.0, causal=False)
+    assert_within(out, ref, tol)
+    assert_within(lse, ref_lse, tol_l)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_millions_of_empty_sequences_between_prompts(d):
+    """The block that goes from the 20th prompt to the next passes 12 million
+    sequences without new tokens (the shares cut neither place)."""
+    kvh, group, page, gap = 2, 4, 1024, 12_000_000
+    q_lens = [200 + 37 * i % 120 for i in range(48)]
+    kv_lens = [300 + 17 * i for i in range(48)]
+    kp, vp, table, K, V = make_cache(kv_lens, kvh, d, page, 5)
+    at = np.arange(48) + gap * (np.arange(48) >= 20)
+    batch = 48 + gap
+    new, kv = np.zeros(batch, dtype=np.int64), np.zeros(batch, dtype=np.int32)
+    new[at], kv[at] = q_lens, kv_lens
+    wide = torch.full((batch, table.shape[1]), -1, dtype=torch.int32)
+    wide[torch.as_tensor(at)] = table
+    n = sum(q_lens)
+    q = randn(n, kvh * group, d, seed=6)
+    out, lse = torch.empty_like(q, device=DEV), torch.empty(n, kvh * group, device=DEV)
+    ws = hq.alloc_paged_attention_workspace(batch, n, max(q_lens), max(kv_lens), kvh, group, d)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    hq.hq_paged_attention(q.to(DEV), starts(new).to(DEV), torch.as_tensor(kv).to(DEV), hq.Pages(kp.to(DEV), vp.to(DEV)),
+                          wide.to(DEV), d ** -0.5, out, ws, max_q=max(q_lens), max_kv=max(kv_lens), lse=lse, status=status)
+    assert int(status) == 0
+    ref, ref_lse, tol, _, tol_l = attend(q, K, V, q_lens, d ** -0.5)
     assert_within(out, ref, tol)
     assert_within(lse, ref_lse, tol_l)
