@@ -20,7 +20,24 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libhq.so")
 if not os.path.exists(_LIB_PATH):
     raise ImportError(f"{_LIB_PATH} is missing: build it with "
                       "`python -c 'import __graft_entry__ as g; g.build()'`")
-from . import _hq_torch  # noqa: E402  (the serving operators' calls; built beside libhq.so)
+
+
+class _Missing:
+    """In the place of the serving operators' extension where it cannot be loaded:
+    the codec does without it, every call that needs it raises."""
+
+    def __init__(self, why: Exception):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"the serving operators' extension did not load ({self._why}): build it with "
+                          "`python -c 'import __graft_entry__ as g; g.build()'`")
+
+
+try:
+    from . import _hq_torch  # noqa: E402  (the serving operators' calls; built beside libhq.so)
+except ImportError as e:
+    _hq_torch = _Missing(e)
 
 HQ_Z, HQ_A2, HQ_D4, HQ_E8 = 1, 2, 4, 8
 HQ_BF16, HQ_F32 = 0, 1
@@ -150,7 +167,8 @@ class HQError(RuntimeError):
         self.code = code
 
 
-_hq_torch.set_error(HQError)
+if not isinstance(_hq_torch, _Missing):
+    _hq_torch.set_error(HQError)
 
 
 def library():
