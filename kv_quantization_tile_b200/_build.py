@@ -1,17 +1,19 @@
 """Build the sm_100a codec library (``libhq.so``) in-tree with nvcc, and the
-extension through which Python calls the serving operators (``_hq_torch.so``)
-with g++.
+extension through which Python calls the serving operators
+(``_hq_torch-<python>-<torch>.so``) with g++.
 
 Each ``csrc/*.cu`` file is compiled to an object in parallel, then linked
 into ``kv_quantization_tile_b200/libhq.so`` with the CUDA runtime linked
 statically; ``csrc/hq_torch.cpp`` is compiled against torch's headers and linked
 to that library.  The build is skipped when both are newer than every source
-and header.
+and header; an extension built for another torch or Python has another name, so
+it is neither loaded nor taken for this one.
 """
 from __future__ import annotations
 
 import glob
 import os
+import re
 import subprocess
 import sys
 import sysconfig
@@ -22,11 +24,17 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libhq.so")
-EXT = os.path.join(PKG, "_hq_torch.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
                 "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
+
+
+def ext_path() -> str:
+    """The extension for this Python and this torch, whose binary interfaces it uses."""
+    import torch
+    key = f"{sysconfig.get_config_var('SOABI')}-torch-{torch.__version__}-abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+    return os.path.join(PKG, f"_hq_torch-{re.sub('[^A-Za-z0-9.+-]', '_', key)}.so")
 
 
 def _sources():
@@ -39,9 +47,10 @@ def _deps():
 
 
 def stale() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(EXT)):
+    ext = ext_path()
+    if not (os.path.exists(LIB) and os.path.exists(ext)):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
+    t = min(os.path.getmtime(LIB), os.path.getmtime(ext))
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
@@ -75,10 +84,11 @@ def _compile_ext() -> str:
 
 def _link_ext(obj: str):
     from torch.utils import cpp_extension
-    tmp = EXT + f".tmp{os.getpid()}"
+    ext = ext_path()
+    tmp = ext + f".tmp{os.getpid()}"
     _run(["g++", "-shared", "-o", tmp, obj, LIB, *[f"-L{p}" for p in cpp_extension.library_paths()], "-lc10", "-lc10_cuda",
-          "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], "link of _hq_torch.so")
-    os.replace(tmp, EXT)
+          "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], "link of the extension")
+    os.replace(tmp, ext)
 
 
 def build(force: bool = False, ptxas_verbose: bool = False) -> str:

@@ -9,12 +9,16 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
 import os
 from dataclasses import dataclass
 
 import numpy as np
 import torch
+
+from ._build import ext_path
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libhq.so")
 if not os.path.exists(_LIB_PATH):
@@ -34,10 +38,22 @@ class _Missing:
                           "`python -c 'import __graft_entry__ as g; g.build()'`")
 
 
-try:
-    from . import _hq_torch  # noqa: E402  (the serving operators' calls; built beside libhq.so)
-except ImportError as e:
-    _hq_torch = _Missing(e)
+def _load_extension():
+    """The serving operators' calls, built beside libhq.so for this Python and torch."""
+    path = ext_path()
+    name = __package__ + "._hq_torch"
+    try:
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is missing")
+        spec = importlib.util.spec_from_file_location(name, path, loader=importlib.machinery.ExtensionFileLoader(name, path))
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        return module
+    except ImportError as e:
+        return _Missing(e)
+
+
+_hq_torch = _load_extension()
 
 HQ_Z, HQ_A2, HQ_D4, HQ_E8 = 1, 2, 4, 8
 HQ_BF16, HQ_F32 = 0, 1

@@ -5,8 +5,11 @@ import subprocess
 import sys
 
 import pytest
+import torch
 
 import kv_quantization_tile_b200
+from kv_quantization_tile_b200 import _build, hq
+from kv_quantization_tile_b200._build import ext_path
 
 PKG = os.path.dirname(os.path.abspath(kv_quantization_tile_b200.__file__))
 
@@ -50,6 +53,20 @@ def test_the_codec_does_without_the_extension(bare):
 
 
 def test_an_extension_that_does_not_load_counts_as_missing(bare):
-    (bare / "_hq_torch.so").write_bytes(b"not a library")
+    (bare / os.path.basename(ext_path())).write_bytes(b"not a library")
     r = python(bare, USE)
     assert r.returncode == 0 and "fine" in r.stdout, r.stderr
+
+
+def test_an_extension_for_another_torch_is_neither_loaded_nor_kept(bare, monkeypatch):
+    ours = ext_path()
+    assert os.path.samefile(hq._hq_torch.__file__, ours)
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    theirs = ext_path()
+    assert theirs != ours and _build.stale()  # built again for the torch that is there
+    os.symlink(ours, bare / os.path.basename(theirs))
+    r = python(bare, USE)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr
+    os.symlink(ours, bare / os.path.basename(ours))
+    r = python(bare, USE)
+    assert r.returncode != 0 and "CUDA tensors only" in r.stderr  # loaded: it looks at the tensors
