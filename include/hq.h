@@ -508,7 +508,7 @@ int hq_paged_attention_workspace_bytes(int64_t batch, int64_t tokens, int64_t ma
  *                whatever they hold; vectors within it should be finite (a
  *                NaN or infinity may reach every row of the same sequence and
  *                KV head, masked or not).
- *   scale        finite, any sign
+ *   scale        below 2.3e38 in magnitude, any sign
  *   causal       0: every new token sees all kv_len tokens (window still
  *                counts from its position)
  *   out          [tokens][heads * group][head_dim], HQ_BF16 or HQ_F32

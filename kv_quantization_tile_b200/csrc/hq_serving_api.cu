@@ -248,7 +248,8 @@ static int paged_attention(const hq_rows *q, const int32_t *q_start, const int32
     if (rc) return rc;
     rc = check_paged_sizes(batch, tokens, max_q, max_kv, pages->heads, pages->head_dim, group);
     if (rc) return rc;
-    if (!std::isfinite(scale) || window < 0 || table_width < 0 || (batch > 1 && table_stride < table_width))
+    const float scale_log2 = std::fabs(scale) * 1.44269504088896341f;  // infinite past 2.36e38
+    if (!std::isfinite(scale_log2) || window < 0 || table_width < 0 || (batch > 1 && table_stride < table_width))
         return HQ_ERR_ARG;
     if (batch == 0 || tokens == 0 || max_q == 0) return HQ_OK;
     const int heads = pages->heads * group, d = pages->head_dim;
@@ -281,7 +282,7 @@ static int paged_attention(const hq_rows *q, const int32_t *q_start, const int32
     a.slot_stride = pages->slot_stride;
     a.pages = (uint32_t)pages->pages;
     a.page_shift = log2_of(pages->page_size);
-    a.scale_log2 = scale == 0.0f ? 1.0f : std::fabs(scale) * 1.44269504088896341f;
+    a.scale_log2 = scale == 0.0f ? 1.0f : scale_log2;
     a.q_mode = scale == 0.0f ? 2 : scale < 0.0f ? 1 : 0;
     a.causal = causal != 0;
     a.window = (int)(window > INT32_MAX ? 0 : window);  // wider than any cache: all

@@ -249,3 +249,9 @@ def test_cpu_tensors_and_wrong_shapes_are_refused():
         hq.hq_paged_attention(x[:, :3], i32(0, 1, 2), i32(1, 1), pool, i32(0, 1).view(2, 1), 0.1, x[:, :3], ws, **args)
     with pytest.raises(ValueError):
         hq.hq_attention_merge(x, torch.zeros(2, 4), x, torch.zeros(2, 3), x)
+
+
+@pytest.mark.parametrize("scale", [2.4e38, -3.4e38])
+def test_attention_refuses_scales_past_the_range_of_its_exponents(scale):
+    """The kernels work in powers of two: scale log2 e has to be finite too."""
+    assert attention(scale=scale) == hq.HQ_ERR_ARG
