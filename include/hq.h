@@ -507,7 +507,8 @@ int hq_paged_attention_workspace_bytes(int64_t batch, int64_t tokens, int64_t ma
  *                and raises HQ_ST_INDEX.  Slots past kv_len are never used,
  *                whatever they hold; vectors within it should be finite (a
  *                NaN or infinity may reach every row of the same sequence and
- *                KV head, masked or not).
+ *                KV head, masked or not), those of V up to 2^70 in magnitude
+ *                (a row's binary32 sum holds 2^30 of them at weights of 2^24).
  *   scale        below 2.3e38 in magnitude, any sign
  *   causal       0: every new token sees all kv_len tokens (window still
  *                counts from its position)
