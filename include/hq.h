@@ -493,7 +493,8 @@ int hq_paged_attention_workspace_bytes(int64_t batch, int64_t tokens, int64_t ma
  * over the cached tokens t with t <= p (causal) and t > p - window (window >
  * 0).  A row that sees no token is zero with lse minus infinity.  Products run
  * on the tensor cores with bf16 operands and binary32 sums; the weights are
- * rounded to bf16 for the product with v, their sum is not.
+ * rounded to bf16 for the product with v, their sum in lse is not, and the one
+ * that divides the product only in what a rounding of a dominating weight adds.
  *   q            bf16 [tokens][heads * group][head_dim]
  *   q_start      device int32 [batch + 1], non-decreasing, within 0 .. tokens;
  *                rows of out outside every sequence are left as they were

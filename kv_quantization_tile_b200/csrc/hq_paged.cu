@@ -724,11 +724,11 @@ PagedPlan paged_plan(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_k
         at += (bytes + 255) / 256 * 256;
         return o;
     };
-    auto place = [&](PagedShare &k, int parts) {
+    auto place = [&](PagedShare &k, int parts, int sums) {  // sums: floats of a row of a part beside its output
         k.prefix = take(8 * (uint64_t)(batch + 1));
         k.start = take(sizeof(PagedStart) * (uint64_t)k.grid);
         k.counter = take(4 * (uint64_t)k.grid * parts);
-        k.part = take(2 * (uint64_t)k.grid * k.rows * (head_dim + 2) * 4);
+        k.part = take(2 * (uint64_t)k.grid * k.rows * (head_dim + sums) * 4);
     };
     // tokens a job reads (any window up to INT64_MAX; max_q <= 2^30)
     const int64_t reach = window > 0 && window < max_kv - max_q ? window + max_q : max_kv;
@@ -762,14 +762,14 @@ PagedPlan paged_plan(int64_t batch, int64_t tokens, int64_t max_q, int64_t max_k
         }
         // by shares: at most 32 parts of a job on average, which one block joins
         if (!many && !p.few.split && 32 * jobs < p.few.grid) p.few.grid = (int)(32 * jobs > 0 ? 32 * jobs : 1);
-        if (!p.few.split) place(p.few, 1);
+        if (!p.few.split) place(p.few, 1, 2);
     }
     if (many) {
         p.many.rows = paged_many_rows(head_dim);
         p.many.row_lo = batch > 1 ? 16 : 0;
         p.many.row_hi = INT32_MAX;
         p.many.grid = sm_count();
-        place(p.many, p.many.rows / 128);
+        place(p.many, p.many.rows / 128, 3);
     }
     p.total = at > 256 ? at : 256;
     return p;

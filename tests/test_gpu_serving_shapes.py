@@ -137,6 +137,39 @@ def test_values_at_the_end_of_their_range(d, q_lens, kv_lens, out_dtype):
     assert_within(out, ref, tol_b if out_dtype == BF else tol_f)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("q_len", [1, 512])
+def test_rows_that_one_token_dominates(d, q_len):
+    """A token 22 to 23 powers of two above all others is its row's output, but
+    for their share S of the weights: that weight's rounding to bf16 (2^-8 of it at
+    most) is in numerator and denominator alike, also where the running maximum
+    was taken from earlier tiles.  What is left: the others' roundings and score
+    errors, (UB + e) S each, e as in attend() below 2^-8, and 4 (n + 512) U32 of
+    the sums."""
+    kvh, group, page, kv, at = 8, 4, 64, 2048, 1500
+    kp, vp, table, K, V = make_cache([kv], kvh, d, page, 3)
+    K[0] = torch.zeros(kv, kvh, d, dtype=BF)
+    K[0][at] = 1.0
+    V[0][at] = torch.where(torch.arange(d) % 2 == 0, 4.0, -4.0).to(BF)
+    for pool, x in ((kp, K[0]), (vp, V[0])):
+        for i in range(kv // page):
+            pool[int(table[0, i])] = x[i * page:(i + 1) * page].transpose(0, 1)
+    # scores of 15.5 to 16 at the token, 0 elsewhere
+    q = (torch.linspace(15.5, 16, q_len * kvh * group).view(q_len, kvh * group, 1) * torch.ones(d)).to(BF)
+    scale = 1.0 / d
+    out, lse = torch.empty(q.shape, dtype=F32, device=DEV), torch.empty(q.shape[:2], device=DEV)
+    ws = hq.alloc_paged_attention_workspace(1, q_len, q_len, kv, kvh, group, d)
+    hq.hq_paged_attention(q.to(DEV), starts([q_len]).to(DEV), torch.tensor([kv], dtype=torch.int32, device=DEV),
+                          hq.Pages(kp.to(DEV), vp.to(DEV)), table.to(DEV), scale, out, ws, max_q=q_len, max_kv=kv,
+                          causal=False, lse=lse)
+    ref, ref_lse, _, _, tol_l = attend(q, K, V, [q_len], scale, causal=False)
+    share = (kv - 1) / (torch.exp(q[..., 0].double()) + kv - 1)
+    big = V[0].double().abs().max()
+    tol = (2 * (UB + 2.0 ** -8) * share + 4 * (kv + 512) * U32) * big
+    assert_within(out, ref, tol[..., None].expand_as(ref))
+    assert_within(lse, ref_lse, tol_l)
+
+
 # ----------------------------------------------------------------- rotation
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 @pytest.mark.parametrize("din,dout", [(BF, BF), (F32, F32), (F32, BF), (BF, F32)])
