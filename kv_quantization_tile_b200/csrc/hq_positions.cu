@@ -17,9 +17,12 @@
 // heads of q, k and v alike.  The 16 are four quads of 4 elements so placed
 // that a warp's stores are contiguous: pairs of adjacent quads, 16 bytes, where
 // the output is bf16; quads on their own, 16 bytes, where it is binary32 (8191 x
-// 32 x 128 in binary32: 45.7 us, with adjacent quads, half a sector per store,
-// 53.3; 8192 tokens of 48 heads from binary32 to bf16 the other way round, 55.2
-// against 51.2).
+// 32 x 128 in binary32: 45.5 us, with adjacent quads, half a sector per store,
+// 53.1; 8192 tokens of 48 heads from binary32 to bf16 the other way round, 55.2
+// against 51.2).  The two pairs of adjacent quads lie 8 elements apart, a whole
+// item in a row, unless they have to hold pairs half the rotated part apart: half
+// a head apart everywhere, and with the addresses that takes, the same 8192
+// tokens take 53.3 us, from bf16 to bf16 45.2 against 40.1.
 #include "hq_paged.h"
 
 namespace hq {
@@ -34,12 +37,11 @@ __device__ __forceinline__ void unpack(uint32_t w, float &lo, float &hi)
     hi = __uint_as_float(w & 0xffff0000u);
 }
 
-// The quads of item j of a span of n elements that begins at `base`
-template <bool QUADS>
-__device__ __forceinline__ void places(int base, int n, int j, int (&at)[4])
+// The quads of item j of a span of n elements that begins at `base`, a quarter apart
+__device__ __forceinline__ void quarters(int base, int n, int j, int (&at)[4])
 {
 #pragma unroll
-    for (int q = 0; q < 4; q++) at[q] = base + (QUADS ? q * (n / 4) + 4 * j : (q >> 1) * (n / 2) + 8 * j + 4 * (q & 1));
+    for (int q = 0; q < 4; q++) at[q] = base + q * (n / 4) + 4 * j;
 }
 
 template <bool QUADS>
@@ -130,7 +132,7 @@ __global__ void __launch_bounds__(kPosThreads) positions_kernel(const PosArgs a)
     const int items = (a.heads + 2 * a.kvh) * units;
     const int64_t tok0 = (int64_t)blockIdx.x * a.tokens_per_block;
     const int nt = (int)min((int64_t)a.tokens_per_block, a.tokens - tok0);
-    const int gshift = (QUADS ? 1 : 0) + (a.interleaved ? 1 : 0);  // log2 of the groups
+    const int gshift = !QUADS ? 0 : a.interleaved ? 2 : 1;  // log2 of the groups
 
     for (int e = tid; e < nt * pairs; e += kPosThreads) {
         const int t = e / pairs, i = e - t * pairs;
@@ -152,10 +154,16 @@ __global__ void __launch_bounds__(kPosThreads) positions_kernel(const PosArgs a)
         const int64_t tok = tok0 + t;
         const bool rotated = j < runits && head < a.heads + a.kvh;
         int at[4];
-        // the rotated span of a head, the rest of it, or all of a value's
-        if (head >= a.heads + a.kvh) places<QUADS>(0, a.head_dim, j, at);
-        else if (rotated) places<QUADS>(0, a.rotary, j, at);
-        else places<QUADS>(a.rotary, a.head_dim - a.rotary, j - runits, at);
+        if constexpr (QUADS) {  // the rotated span of a head, or the rest of it (no append)
+            if (rotated) quarters(0, a.rotary, j, at);
+            else quarters(a.rotary, a.head_dim - a.rotary, j - runits, at);
+        } else {
+            const bool half = rotated && !a.interleaved;
+            at[0] = half ? 8 * j : 16 * j;
+            at[2] = half ? a.rotary / 2 + 8 * j : 16 * j + 8;
+            at[1] = at[0] + 4;
+            at[3] = at[2] + 4;
+        }
         int64_t slot = 0;
         if (a.slots) {
             slot = a.slots[tok];
