@@ -554,8 +554,9 @@ int hq_test_paged_attention_stalled(const hq_rows *q, const int32_t *q_start, co
  *            multiple of 8 up to 1024; lse_a, lse_b, lse fp32 [tokens][heads]
  *            (lse may be NULL).  A part whose lse is minus infinity counts
  *            for nothing, whatever it holds; if both are, the row is zero.  out may be a or b themselves
- *            (same strides and type); lse must be neither lse_a nor lse_b
- *            (HQ_ERR_ARG: other threads still read them).
+ *            (same strides and type); lse must not overlap lse_a or lse_b
+ *            (HQ_ERR_ARG: other threads still read them); any other overlap is
+ *            undefined.
  * tokens * heads < 2^32. */
 int hq_attention_merge(const hq_rows *a, const float *lse_a, const hq_rows *b, const float *lse_b,
                        int64_t tokens, int heads, int head_dim, const hq_rows *out, float *lse,

@@ -322,7 +322,10 @@ int hq_attention_merge(const hq_rows *a, const float *lse_a, const hq_rows *b, c
     if (!readable(a, tokens, heads) || !readable(b, tokens, heads) || !writable(out, tokens, heads, head_dim))
         return HQ_ERR_ARG;
     if (!lse_a || !lse_b || !aligned(lse_a, 4) || !aligned(lse_b, 4) || !aligned(lse, 4)) return HQ_ERR_ARG;
-    if (lse && (lse == lse_a || lse == lse_b)) return HQ_ERR_ARG;
+    // rows of lse are written while other threads still read these
+    const uint64_t bytes = 4 * (uint64_t)tokens * heads;
+    auto apart = [&](const float *r) { return (uintptr_t)lse + bytes <= (uintptr_t)r || (uintptr_t)r + bytes <= (uintptr_t)lse; };
+    if (lse && !(apart(lse_a) && apart(lse_b))) return HQ_ERR_ARG;
     MergeArgs m{};
     m.a = rows_of(a, tokens, heads);
     m.b = rows_of(b, tokens, heads);

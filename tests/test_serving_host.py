@@ -255,3 +255,9 @@ def test_cpu_tensors_and_wrong_shapes_are_refused():
 def test_attention_refuses_scales_past_the_range_of_its_exponents(scale):
     """The kernels work in powers of two: scale log2 e has to be finite too."""
     assert attention(scale=scale) == hq.HQ_ERR_ARG
+
+
+@pytest.mark.parametrize("lse", [A + 4, A + 124, A + 4096 - 4, A + 4096 + 124])
+def test_merge_refuses_an_lse_that_overlaps_those_it_reads(lse):
+    """4 x 8 rows: 128 bytes from A and from A + 4096 are read."""
+    assert merge(lse=lse) == hq.HQ_ERR_ARG
